@@ -54,9 +54,10 @@ def listed():
         # The up projection of a training step.
         {"name": "matmul_forward", "op": "matmul", "m": 16384, "n": 11008, "k": 4096, "block_rows": 128, "type": "bf16",
          "codes": "e4m3"},
-        # Its weight gradient over a ragged batch of tokens, both operands scaled along the tokens.
+        # Its weight gradient over a ragged batch of tokens, both operands scaled along the tokens, as the bf16
+        # contribution that the gradient reduction takes.
         {"name": "matmul_weight_gradient", "op": "matmul", "m": 11008, "n": 4096, "k": 8111, "block_rows": 1,
-         "type": "fp32", "codes": "e5m2"},
+         "type": "bf16", "codes": "e5m2"},
     ]
 
 
