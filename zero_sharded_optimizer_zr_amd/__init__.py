@@ -2,7 +2,8 @@
 an AMD Instinct MI355X.
 
 Argument marshalling only.  Every function has the name of the C entry point
-it calls (declared in ``include/zr.h``); every step of the path runs in the
+it calls (declared in ``include/zr.h``, the 8-bit floating-point operators in
+``include/zr_fp8.h``); every step of the path runs in the
 library's HIP kernels.  PyTorch provides device memory (``torch.Tensor``) and
 streams.  Importing fails loudly if ``libzr.so`` has not been built.
 
@@ -28,6 +29,8 @@ __all__ = [
     "zr_unpack_int4", "zr_host_simd", "zr_host_adamw_step", "offload_staging", "zr_offload_adamw_step",
     "zr_graph_capture_begin", "zr_graph_capture_end", "zr_graph_info", "zr_graph_set_adamw", "zr_graph_launch",
     "zr_graph_destroy", "zr_last_error", "zr_abi_version", "LIBRARY", "SYMBOLS",
+    "zr_quantize_fp8", "zr_matmul_fp8", "zr_rmsnorm_fp8", "zr_rmsnorm_backward", "fp8_matrix", "rmsnorm_workspace",
+    "FP8_SYMBOLS", "ZR_FP8_GROUP", "ZR_RMSNORM_PARTIALS",
 ]
 
 LIBRARY = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libzr.so")
@@ -106,12 +109,20 @@ _SIGS = {
     "zr_last_error": ([], ctypes.c_char_p),
     "zr_abi_version": ([], _I32),
 }
-for _name, (_args, _res) in _SIGS.items():
+_FP8_SIGS = {
+    "zr_quantize_fp8": ([_P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _P], _I32),
+    "zr_matmul_fp8": ([_P, _I64, _P, _I32, _P, _I64, _P, _I32, _I64, _I64, _I64, _P, _I32, _I64, _I32, _P], _I32),
+    "zr_rmsnorm_fp8": ([_P, _I64, _P, _I64, _P, _I32, _I64, _I64, ctypes.c_double, _P, _I64, _P, _I64, _P, _I64, _P,
+                        _P, _P], _I32),
+    "zr_rmsnorm_backward": ([_P, _I64, _P, _I64, _P, _P, _P, _I64, _I32, _I64, _I64, _P, _I64, _P, _P, _P], _I32),
+}
+for _name, (_args, _res) in (_SIGS | _FP8_SIGS).items():
     _f = getattr(_lib, _name)
     _f.argtypes = _args
     _f.restype = _res
 
-SYMBOLS = tuple(_SIGS)
+SYMBOLS = tuple(_SIGS)          # zr.h
+FP8_SYMBOLS = tuple(_FP8_SIGS)  # zr_fp8.h
 
 
 def zr_last_error() -> str:
@@ -611,3 +622,155 @@ def zr_graph_destroy(g: Graph) -> None:
         _lib.zr_graph_destroy(g._h)
         g._h = ctypes.c_void_p(None)
 
+
+# ------------------------------------------ 8-bit floating-point operators ----
+
+ZR_FP8_GROUP = 128
+ZR_RMSNORM_PARTIALS = 512
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_FORMATS = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+_SCALES = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _shape(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() not in (1, 2):
+        raise ValueError(f"{name} must have one or two dimensions")
+    return (1, t.shape[0]) if t.dim() == 1 else tuple(t.shape)
+
+
+def _matrix(t: Optional[torch.Tensor], dtypes, name: str, shape: Optional[Tuple[int, int]] = None):
+    """(address, row distance) of a matrix with contiguous rows: a 2-D tensor, or
+    a 1-D tensor as one row.  (None, 0) for None."""
+    if t is None:
+        return None, 0
+    rows, cols = _shape(t, name)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} is {rows} x {cols}, {shape[0]} x {shape[1]} needed")
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        return t.data_ptr() or None, cols
+    if t.stride(0) < cols:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return t.data_ptr() or None, t.stride(0)
+
+
+def _vector(t: Optional[torch.Tensor], dtypes, n: int, name: str) -> Optional[int]:
+    """Address of a contiguous tensor of at least n elements."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements, {n} needed")
+    return t.data_ptr() or None
+
+
+def _groups(n: int) -> int:
+    return -(-n // ZR_FP8_GROUP)
+
+
+def fp8_matrix(rows: int, cols: int, dtype=torch.float8_e4m3fn, block_rows: int = 1,
+               device=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(codes [rows, cols], scales) for the 8-bit operators, uninitialised; the
+    rows of codes start on 128-byte lines, so that every kernel takes its vector path."""
+    device = device if device is not None else "cuda"
+    codes = torch.empty(rows, _groups(cols) * ZR_FP8_GROUP, dtype=dtype, device=device)[:, :cols]
+    tall = rows if block_rows == 1 else _groups(rows)
+    return codes, torch.empty(tall, _groups(cols), dtype=torch.float8_e8m0fnu, device=device)
+
+
+def rmsnorm_workspace(cols: int, device=None) -> torch.Tensor:
+    """Workspace of zr_rmsnorm_backward for rows of `cols` elements."""
+    return torch.empty(ZR_RMSNORM_PARTIALS, cols, dtype=torch.float32, device=device if device is not None else "cuda")
+
+
+def zr_quantize_fp8(src: torch.Tensor, q: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                    qt: Optional[torch.Tensor] = None, scales_t: Optional[torch.Tensor] = None, *,
+                    block_rows: int = 1, stream=None) -> None:
+    """e4m3 or e5m2 codes (q's dtype) of src [rows, cols] (bf16 or fp16) and E8M0
+    scales: one per 128 of a row (block_rows 1; qt, scales_t are the codes and scales
+    of src's transpose) or per 128 x 128 block (block_rows 128; qt, scales_t are the
+    transposes of q, scales).  Either pair may be left out."""
+    rows, cols = _shape(src, "src")
+    p_src, ld = _matrix(src, (torch.bfloat16, torch.float16), "src")
+    p_q, ldq = _matrix(q, _FORMATS, "q", (rows, cols))
+    p_qt, ldqt = _matrix(qt, _FORMATS, "qt", (cols, rows))
+    if q is not None and qt is not None and q.dtype != qt.dtype:
+        raise TypeError("q and qt must have one dtype")
+    one = q if q is not None else qt
+    if one is None:
+        raise ValueError("neither q nor qt given")
+    down, across = (rows, cols) if block_rows == 1 else (_groups(rows), _groups(cols))
+    p_s = _vector(scales, _SCALES, down * _groups(cols), "scales")
+    p_st = _vector(scales_t, _SCALES, across * _groups(rows), "scales_t")
+    _gpu_call(_lib.zr_quantize_fp8, stream, (src, q, scales, qt, scales_t), p_src, _DTYPES[src.dtype], rows, cols, ld,
+              int(block_rows), _FORMATS[one.dtype], p_q, ldq, p_s, p_qt, ldqt, p_st)
+
+
+def zr_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
+                  out: torch.Tensor, *, b_block_rows: int = 1, accumulate: bool = False, stream=None) -> None:
+    """out [m, n] (bf16, fp16 or fp32) = A B^T for codes a [m, k] (e4m3 or e5m2) with a
+    scale per 128 of a row and b [n, k] (e4m3) with a scale per 128 of a row
+    (b_block_rows 1) or per 128 x 128 block (128); accumulate adds to out."""
+    (m, k), (n, kb) = _shape(a, "a"), _shape(b, "b")
+    if k != kb:
+        raise ValueError(f"a has rows of {k} codes, b of {kb}")
+    p_a, lda = _matrix(a, _FORMATS, "a")
+    p_b, ldb = _matrix(b, (torch.float8_e4m3fn,), "b")
+    p_out, ldo = _matrix(out, _DTYPES, "out", (m, n))
+    p_sa = _vector(a_scales, _SCALES, m * _groups(k), "a_scales")
+    p_sb = _vector(b_scales, _SCALES, (n if b_block_rows == 1 else _groups(n)) * _groups(k), "b_scales")
+    _gpu_call(_lib.zr_matmul_fp8, stream, (a, a_scales, b, b_scales, out), p_a, lda, p_sa, _FORMATS[a.dtype], p_b, ldb,
+              p_sb, int(b_block_rows), m, n, k, p_out, _DTYPES[out.dtype], ldo, int(bool(accumulate)))
+
+
+def zr_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, y: Optional[torch.Tensor] = None,
+                   q: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, *,
+                   residual: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                   rstd: Optional[torch.Tensor] = None, eps: float = 1e-5, stream=None) -> None:
+    """h = x + residual (rounded to x's dtype; h = x without residual), y = h / rms(h)
+    * weight, q and scales = e4m3 codes of y with a scale per 128 of a row, rstd =
+    1 / rms(h) in fp32.  h, rstd and one of y and (q, scales) may be left out; h may be
+    x or residual."""
+    rows, cols = shape = _shape(x, "x")
+    kinds = (torch.bfloat16, torch.float16)
+    p_x, ldx = _matrix(x, kinds, "x")
+    same = (x.dtype,)
+    p_r, ldr = _matrix(residual, same, "residual", shape)
+    p_h, ldh = _matrix(h, same, "h", shape)
+    p_y, ldy = _matrix(y, same, "y", shape)
+    p_q, ldq = _matrix(q, (torch.float8_e4m3fn,), "q", shape)
+    p_w = _vector(weight, same, cols, "weight")
+    p_s = _vector(scales, _SCALES, rows * _groups(cols), "scales")
+    p_rstd = _vector(rstd, (torch.float32,), rows, "rstd")
+    _gpu_call(_lib.zr_rmsnorm_fp8, stream, (x, residual, weight, h, y, q, scales, rstd), p_x, ldx, p_r, ldr, p_w,
+              _DTYPES[x.dtype], rows, cols, float(eps), p_h, ldh, p_y, ldy, p_q, ldq, p_s, p_rstd)
+
+
+def zr_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                        dx: torch.Tensor, dweight: torch.Tensor, workspace: torch.Tensor, *,
+                        dh: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of zr_rmsnorm_fp8: dx (of x and of residual alike, dh added) and
+    dweight, from dy, the forward pass's h (x if it had no residual) and rstd, through
+    a workspace of rmsnorm_workspace(cols).  dx may be dy or dh."""
+    rows, cols = shape = _shape(h, "h")
+    p_h, ldh = _matrix(h, (torch.bfloat16, torch.float16), "h")
+    same = (h.dtype,)
+    p_dy, lddy = _matrix(dy, same, "dy", shape)
+    p_dh, lddh = _matrix(dh, same, "dh", shape)
+    p_dx, lddx = _matrix(dx, same, "dx", shape)
+    p_w, p_dw = _vector(weight, same, cols, "weight"), _vector(dweight, same, cols, "dweight")
+    p_rstd = _vector(rstd, (torch.float32,), rows, "rstd")
+    p_ws = _vector(workspace, (torch.float32,), ZR_RMSNORM_PARTIALS * cols, "workspace")
+    _gpu_call(_lib.zr_rmsnorm_backward, stream, (dy, h, weight, rstd, dx, dweight, workspace, dh), p_dy, lddy, p_h, ldh,
+              p_w, p_rstd, p_dh, lddh, _DTYPES[h.dtype], rows, cols, p_dx, lddx, p_dw, p_ws)

@@ -1,0 +1,354 @@
+// Root-mean-square norm with the residual's addition and 8-bit output, and its
+// backward pass (gfx950).
+//
+// Forward, per row: h = T(x + residual), rstd = 1 / sqrt(mean h^2 + eps),
+// y = h * rstd * weight, and codes of y with one E8M0 scale per 128 columns.
+// Backward, with xh = h * rstd and g = dy * weight: dx = rstd * (g - xh * mean(g xh))
+// + dh and dweight = sum over rows of dy * xh.
+//
+// Sums are fp32: a lane's elements in column order, then the lanes of a wave and
+// the waves of a row in a fixed tree, so results depend only on the inputs, not
+// on the grid.  Both passes are bound by HBM.
+#include "fp8.hpp"
+
+namespace zr {
+
+struct NormArgs {
+    const uint16_t *x, *residual, *weight;
+    int64_t ldx, ldr;
+    int64_t rows, cols;
+    float eps;
+    uint16_t *h, *y;
+    int64_t ldh, ldy;
+    uint8_t *q, *scales;
+    int64_t ldq;
+    float *rstd;
+};
+
+// Eight elements of the stream h (fp32, already rounded to T).
+template <typename T>
+__device__ __forceinline__ u32x4 stream8(u32x4 x, u32x4 r)
+{
+    u32x4 h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = T::pack(T::lo(x[i]) + T::lo(r[i]), T::hi(x[i]) + T::hi(r[i]));
+    return h;
+}
+
+template <typename T>
+__device__ __forceinline__ float squares8(u32x4 h, float sum)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sum = __builtin_fmaf(T::lo(h[i]), T::lo(h[i]), sum);
+        sum = __builtin_fmaf(T::hi(h[i]), T::hi(h[i]), sum);
+    }
+    return sum;
+}
+
+__device__ __forceinline__ float rstd_of(float sum, int64_t cols, float eps)
+{
+    return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, (float)cols) + eps));
+}
+
+// y, codes and scales of eight columns from c on (n of them inside the row),
+// held by a lane of the row of 16 lanes that holds the group.
+template <typename T, bool kAligned>
+__device__ __forceinline__ void norm_outputs(const NormArgs &a, int64_t row, int64_t c, int64_t n, u32x4 h, u32x4 w,
+                                             float rstd)
+{
+    float y[kVec];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[2 * i] = T::lo(h[i]) * rstd * T::lo(w[i]);
+        y[2 * i + 1] = T::hi(h[i]) * rstd * T::hi(w[i]);
+    }
+    if (a.y) {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = T::pack(y[2 * i], y[2 * i + 1]);
+        store8<kAligned>(a.y + row * a.ldy + c, o, n);
+    }
+    if (a.q) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            amax = max_u32(amax, __float_as_uint(y[e]) & 0x7fffffffu);
+        const uint32_t s = scale_byte<ZR_E4M3>(group_max(amax));
+        const float inv = inverse_scale(s);
+        store_codes8<kAligned>(a.q + row * a.ldq + c,
+                               u32x2{codes4<ZR_E4M3>(y[0], y[1], y[2], y[3], inv, s),
+                                     codes4<ZR_E4M3>(y[4], y[5], y[6], y[7], inv, s)}, n);
+        if ((threadIdx.x & 15) == 0 && n > 0)
+            a.scales[row * ((a.cols + kGroup - 1) / kGroup) + c / kGroup] = (uint8_t)s;
+    }
+}
+
+// Sum over the workgroup's four waves of a value that wave_sum has spread over
+// each wave; `slot` alternates so that one barrier per sum is enough.
+__device__ __forceinline__ float block_sum(float v, float (*part)[4], int slot)
+{
+    if ((threadIdx.x & 63) == 0)
+        part[slot][threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (part[slot][0] + part[slot][1]) + (part[slot][2] + part[slot][3]);
+}
+
+// Rows of any length and alignment: a workgroup per row, read twice (the second
+// time from cache).  h is written in the second read, so that it may replace x
+// or residual.
+template <typename T, bool kAligned>
+__global__ __launch_bounds__(kBlock) void norm_wide_kernel(NormArgs a)
+{
+    __shared__ float part[2][4];
+    int slot = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, slot ^= 1) {
+        const uint16_t *x = a.x + row * a.ldx, *r = a.residual ? a.residual + row * a.ldr : nullptr;
+        float sum = 0.0f;
+        for (int64_t c = threadIdx.x * kVec; c < a.cols; c += kBlock * kVec) {
+            u32x4 h = load8<kAligned>(x + c, a.cols - c);
+            if (r)
+                h = stream8<T>(h, load8<kAligned>(r + c, a.cols - c));
+            sum = squares8<T>(h, sum);
+        }
+        const float rstd = rstd_of(block_sum(wave_sum(sum), part, slot), a.cols, a.eps);
+        if (a.rstd && threadIdx.x == 0)
+            a.rstd[row] = rstd;
+        // whole rows of 16 lanes stay in the loop: they share a group's maximum
+        for (int64_t c = threadIdx.x * kVec; c - (threadIdx.x & 15) * kVec < a.cols; c += kBlock * kVec) {
+            const int64_t n = a.cols - c;
+            u32x4 h = load8<kAligned>(x + c, n);
+            if (r)
+                h = stream8<T>(h, load8<kAligned>(r + c, n));
+            if (a.h)
+                store8<kAligned>(a.h + row * a.ldh + c, h, n);
+            norm_outputs<T, kAligned>(a, row, c, n, h, load8<kAligned>(a.weight + c, n), rstd);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward --
+
+struct NormGradArgs {
+    const uint16_t *dy, *h, *weight, *dh;
+    const float *rstd;
+    int64_t lddy, ldh, lddh;
+    int64_t rows, cols;
+    uint16_t *dx, *dweight;
+    int64_t lddx;
+    float *partial;  // [groups of rows][cols]
+    int64_t parts;   // groups of rows: row r belongs to group r % parts
+};
+
+// sum of g * h over eight columns (the row's rstd is factored out)
+template <typename T>
+__device__ __forceinline__ float dots8(u32x4 dy, u32x4 w, u32x4 h, float sum)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sum = __builtin_fmaf(T::lo(dy[i]) * T::lo(w[i]), T::lo(h[i]), sum);
+        sum = __builtin_fmaf(T::hi(dy[i]) * T::hi(w[i]), T::hi(h[i]), sum);
+    }
+    return sum;
+}
+
+// dx of eight columns: rstd * (g - h * k) + dh with k = rstd^2 * mean(g h).
+template <typename T>
+__device__ __forceinline__ u32x4 dx8(u32x4 dy, u32x4 w, u32x4 h, u32x4 dh, float rstd, float k)
+{
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = T::pack(__builtin_fmaf(__builtin_fmaf(-k, T::lo(h[i]), T::lo(dy[i]) * T::lo(w[i])), rstd, T::lo(dh[i])),
+                       __builtin_fmaf(__builtin_fmaf(-k, T::hi(h[i]), T::hi(dy[i]) * T::hi(w[i])), rstd, T::hi(dh[i])));
+    return o;
+}
+
+__device__ __forceinline__ float dx_factor(float dot, float rstd, int64_t cols)
+{
+    return __fdiv_rn(dot, (float)cols) * rstd * rstd;
+}
+
+template <typename T, bool kAligned>
+__global__ __launch_bounds__(kBlock) void norm_dx_wide_kernel(NormGradArgs a)
+{
+    __shared__ float part[2][4];
+    int slot = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, slot ^= 1) {
+        const uint16_t *dy = a.dy + row * a.lddy, *h = a.h + row * a.ldh;
+        float sum = 0.0f;
+        for (int64_t c = threadIdx.x * kVec; c < a.cols; c += kBlock * kVec)
+            sum = dots8<T>(load8<kAligned>(dy + c, a.cols - c), load8<kAligned>(a.weight + c, a.cols - c),
+                           load8<kAligned>(h + c, a.cols - c), sum);
+        const float rstd = a.rstd[row];
+        const float k = dx_factor(block_sum(wave_sum(sum), part, slot), rstd, a.cols);
+        for (int64_t c = threadIdx.x * kVec; c < a.cols; c += kBlock * kVec) {
+            const int64_t n = a.cols - c;
+            const u32x4 dh = a.dh ? load8<kAligned>(a.dh + row * a.lddh + c, n) : u32x4{0, 0, 0, 0};
+            store8<kAligned>(a.dx + row * a.lddx + c,
+                             dx8<T>(load8<kAligned>(dy + c, n), load8<kAligned>(a.weight + c, n),
+                                    load8<kAligned>(h + c, n), dh, rstd, k), n);
+        }
+    }
+}
+
+// Partial weight gradients of one column and one group of rows per thread.
+template <typename T>
+__global__ __launch_bounds__(kBlock) void norm_dweight_partial_kernel(NormGradArgs a)
+{
+    const int64_t blocks = (a.cols + kBlock - 1) / kBlock;
+    for (int64_t i = blockIdx.x; i < blocks * a.parts; i += gridDim.x) {
+        const int64_t p = i / blocks, c = (i - p * blocks) * kBlock + threadIdx.x;
+        if (c >= a.cols)
+            continue;
+        float sum = 0.0f;
+        for (int64_t row = p; row < a.rows; row += a.parts)
+            sum = __builtin_fmaf(widen<T>(a.dy[row * a.lddy + c]), widen<T>(a.h[row * a.ldh + c]) * a.rstd[row], sum);
+        a.partial[p * a.cols + c] = sum;
+    }
+}
+
+// dweight from the partial sums.
+template <typename T>
+__global__ __launch_bounds__(kBlock) void norm_dweight_kernel(NormGradArgs a)
+{
+    for (int64_t c = global_tid(); c < a.cols; c += grid_stride()) {
+        float sum = 0.0f;
+        for (int64_t p = 0; p < a.parts; ++p)
+            sum += a.partial[p * a.cols + c];
+        a.dweight[c] = narrow<T>(sum);
+    }
+}
+
+namespace {
+
+template <typename T>
+zr_status norm_run(const NormArgs &a, bool aligned, hipStream_t st)
+{
+    const dim3 grid = grid_of(a.rows);
+    return aligned ? launch(norm_wide_kernel<T, true>, grid, dim3(kBlock), 0, st, a)
+                   : launch(norm_wide_kernel<T, false>, grid, dim3(kBlock), 0, st, a);
+}
+
+template <typename T>
+zr_status norm_backward_run(const NormGradArgs &a, bool aligned, hipStream_t st)
+{
+    zr_status s = ZR_OK;
+    if (a.rows > 0) {
+        // dweight's partial sums first: dx may replace dy
+        const int64_t blocks = (a.cols + kBlock - 1) / kBlock * a.parts;
+        s = launch(norm_dweight_partial_kernel<T>, grid_of(blocks), dim3(kBlock), 0, st, a);
+        if (s == ZR_OK)
+            s = aligned ? launch(norm_dx_wide_kernel<T, true>, grid_of(a.rows), dim3(kBlock), 0, st, a)
+                        : launch(norm_dx_wide_kernel<T, false>, grid_of(a.rows), dim3(kBlock), 0, st, a);
+    }
+    if (s == ZR_OK)
+        s = launch(norm_dweight_kernel<T>, grid_of((a.cols + kBlock - 1) / kBlock), dim3(kBlock), 0, st, a);
+    return s;
+}
+
+// A matrix of 16-bit elements on 16-byte boundaries in every row.
+bool rows_aligned(const void *p, int64_t ld, int64_t rows) { return !p || (aligned_to(p, 16) && (ld % kVec == 0 || rows <= 1)); }
+
+bool same_matrix(const void *p, int64_t ldp, const void *q, int64_t ldq) { return p == q && ldp == ldq; }
+
+}  // namespace
+}  // namespace zr
+
+using namespace zr;
+
+extern "C" zr_status zr_rmsnorm_fp8(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                                    zr_dtype dtype, int64_t rows, int64_t cols, double eps, void *h, int64_t ldh,
+                                    void *y, int64_t ldy, uint8_t *q, int64_t ldq, uint8_t *scales, float *rstd,
+                                    void *stream)
+{
+    clear_error();
+    const char *who = "zr_rmsnorm_fp8";
+    if (dtype != ZR_BF16 && dtype != ZR_F16)
+        return fail(ZR_EINVAL, "%s: dtype = %d, must be ZR_BF16 or ZR_F16", who, dtype);
+    if (rows < 0 || cols < 1)
+        return fail(ZR_EINVAL, "%s: rows < 0 or cols < 1", who);
+    if (!(eps >= 0.0) || !std::isfinite(eps) || !std::isfinite((float)eps))
+        return fail(ZR_EINVAL, "%s: eps must be finite and >= 0", who);
+    if ((!q) != (!scales))
+        return fail(ZR_EINVAL, "%s: codes without scales or scales without codes", who);
+    if (h && !residual)
+        return fail(ZR_EINVAL, "%s: h without residual (it would equal x)", who);
+    if (rows == 0)
+        return ZR_OK;
+    if (!x || !weight || (!y && !q))
+        return fail(ZR_EINVAL, "%s: NULL x or weight, or neither y nor q", who);
+    int64_t nx, nr = 0, nh = 0, ny = 0, nq = 0;
+    if (!matrix_extent(rows, cols, ldx, 2, &nx) || (residual && !matrix_extent(rows, cols, ldr, 2, &nr)) ||
+        (h && !matrix_extent(rows, cols, ldh, 2, &nh)) || (y && !matrix_extent(rows, cols, ldy, 2, &ny)) ||
+        (q && !matrix_extent(rows, cols, ldq, 1, &nq)))
+        return fail(ZR_EINVAL, "%s: row distance below cols, or a matrix past int64", who);
+    if (!aligned_to(x, 2) || !aligned_to(residual, 2) || !aligned_to(weight, 2) || !aligned_to(h, 2) ||
+        !aligned_to(y, 2) || !aligned_to(rstd, 4))
+        return fail(ZR_EALIGN, "%s: 16-bit matrices must be 2-byte and rstd 4-byte aligned", who);
+    {
+        // outputs first; inputs may overlap one another, and h may be x or residual
+        const void *p[8] = {h, y, q, scales, rstd, x, residual, weight};
+        const int64_t b[8] = {nh, ny, nq, rows * ((cols + kGroup - 1) / kGroup), 4 * rows, nx, nr, 2 * cols};
+        for (int i = 0; i < 5; ++i)
+            for (int j = i + 1; j < 8; ++j) {
+                const bool in_place = i == 0 && ((j == 5 && same_matrix(h, ldh, x, ldx)) ||
+                                                 (j == 6 && same_matrix(h, ldh, residual, ldr)));
+                if (p[i] && p[j] && !in_place && overlaps(p[i], b[i], p[j], b[j]))
+                    return fail(ZR_EINVAL, "%s: an output overlaps another buffer", who);
+            }
+    }
+    const NormArgs a{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(residual),
+                     static_cast<const uint16_t *>(weight), ldx, ldr, rows, cols, (float)eps,
+                     static_cast<uint16_t *>(h), static_cast<uint16_t *>(y), ldh, ldy, q, scales, ldq, rstd};
+    const bool aligned = rows_aligned(x, ldx, rows) && rows_aligned(residual, ldr, rows) && aligned_to(weight, 16) &&
+                         rows_aligned(h, ldh, rows) && rows_aligned(y, ldy, rows) &&
+                         (!q || (aligned_to(q, 8) && (ldq % 8 == 0 || rows == 1)));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return dtype == ZR_BF16 ? norm_run<BF16>(a, aligned, st) : norm_run<F16>(a, aligned, st);
+}
+
+extern "C" zr_status zr_rmsnorm_backward(const void *dy, int64_t lddy, const void *h, int64_t ldh, const void *weight,
+                                         const float *rstd, const void *dh, int64_t lddh, zr_dtype dtype,
+                                         int64_t rows, int64_t cols, void *dx, int64_t lddx, void *dweight,
+                                         float *workspace, void *stream)
+{
+    clear_error();
+    const char *who = "zr_rmsnorm_backward";
+    if (dtype != ZR_BF16 && dtype != ZR_F16)
+        return fail(ZR_EINVAL, "%s: dtype = %d, must be ZR_BF16 or ZR_F16", who, dtype);
+    if (rows < 0 || cols < 1)
+        return fail(ZR_EINVAL, "%s: rows < 0 or cols < 1", who);
+    if (!dweight || !workspace || (rows > 0 && (!dy || !h || !weight || !rstd || !dx)))
+        return fail(ZR_EINVAL, "%s: NULL buffer", who);
+    int64_t ndy = 0, nh = 0, ndh = 0, ndx = 0, nw;
+    if (rows > 0 && (!matrix_extent(rows, cols, lddy, 2, &ndy) || !matrix_extent(rows, cols, ldh, 2, &nh) ||
+                     (dh && !matrix_extent(rows, cols, lddh, 2, &ndh)) || !matrix_extent(rows, cols, lddx, 2, &ndx)))
+        return fail(ZR_EINVAL, "%s: row distance below cols, or a matrix past int64", who);
+    if (!matrix_extent(ZR_RMSNORM_PARTIALS, cols, cols, 4, &nw))
+        return fail(ZR_EINVAL, "%s: workspace past int64", who);
+    if (!aligned_to(dy, 2) || !aligned_to(h, 2) || !aligned_to(weight, 2) || !aligned_to(rstd, 4) ||
+        !aligned_to(dh, 2) || !aligned_to(dx, 2) || !aligned_to(dweight, 2) || !aligned_to(workspace, 4))
+        return fail(ZR_EALIGN, "%s: 16-bit matrices must be 2-byte, rstd and workspace 4-byte aligned", who);
+    {
+        const void *p[8] = {dx, dweight, workspace, dy, h, dh, weight, rstd};
+        const int64_t b[8] = {ndx, 2 * cols, nw, ndy, nh, ndh, rows > 0 ? 2 * cols : 0, 4 * rows};
+        for (int i = 0; i < 3; ++i)
+            for (int j = i + 1; j < 8; ++j) {
+                const bool in_place = i == 0 && ((j == 3 && same_matrix(dx, lddx, dy, lddy)) ||
+                                                 (j == 5 && same_matrix(dx, lddx, dh, lddh)));
+                if (p[i] && p[j] && !in_place && overlaps(p[i], b[i], p[j], b[j]))
+                    return fail(ZR_EINVAL, "%s: an output overlaps another buffer", who);
+            }
+    }
+    const NormGradArgs a{static_cast<const uint16_t *>(dy), static_cast<const uint16_t *>(h),
+                         static_cast<const uint16_t *>(weight), static_cast<const uint16_t *>(dh), rstd, lddy, ldh,
+                         lddh, rows, cols, static_cast<uint16_t *>(dx), static_cast<uint16_t *>(dweight), lddx,
+                         workspace, rows < ZR_RMSNORM_PARTIALS ? rows : ZR_RMSNORM_PARTIALS};
+    const bool aligned = rows_aligned(dy, lddy, rows) && rows_aligned(h, ldh, rows) && aligned_to(weight, 16) &&
+                         rows_aligned(dh, lddh, rows) && rows_aligned(dx, lddx, rows);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return dtype == ZR_BF16 ? norm_backward_run<BF16>(a, aligned, st) : norm_backward_run<F16>(a, aligned, st);
+}
