@@ -150,11 +150,198 @@ __global__ __launch_bounds__(kBlock) void matmul_any_kernel(MatmulArgs p, int64_
     }
 }
 
+// ------------------------------------------------------------- large products --
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kBig = 256;                  // output rows and columns of a workgroup
+constexpr int kBigThreads = 512;           // 8 waves: 2 down the rows x 4 across the columns
+constexpr int kBigStage = 2 * kBig * kGroup;  // LDS bytes of one group of both operands
+
+__device__ __forceinline__ f32x16 multiply32(i32x8 b, int sb, i32x8 a, int sa, f32x16 acc)
+{
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, ZR_E4M3, ZR_E4M3, 0, sb, 0, sa);
+}
+
+// Byte offset of 16-byte piece `piece` (of 8) of row `row` in a staged tile.
+__device__ __forceinline__ int staged(int row, int piece) { return row * kGroup + ((piece ^ (row & 7)) << 4); }
+
+struct ScaleWords {
+    const uint8_t *base;  // of the tile's first row
+    int32_t limit;        // last offset a word may be read at
+};
+
+// Four scale bytes from byte `at` on.
+__device__ __forceinline__ uint32_t scale_word(const ScaleWords &s, int32_t at)
+{
+    const int32_t from = at < s.limit ? at : s.limit;
+    uint32_t w;
+    __builtin_memcpy(&w, s.base + from, 4);
+    return w >> (8 * (at - from));
+}
+
+template <int kFormatA>
+__global__ __launch_bounds__(kBigThreads, 2) void matmul_big_kernel(MatmulArgs p, int64_t tiles_m, int64_t tiles_n)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t stage0[kBigStage], stage1[kBigStage];
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = (wave >> 2) * 128, wn = (wave & 3) * 64, row = lane & 31, half = lane >> 5;
+    const int64_t tiles = tiles_m * tiles_n;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t tm = tile / tiles_n, tn = tile % tiles_n;
+        const int64_t i0 = tm * kBig, j0 = tn * kBig;
+        const int rows_a = (int)(p.m - i0 < kBig ? p.m - i0 : kBig), rows_b = (int)(p.n - j0 < kBig ? p.n - j0 : kBig);
+        const int64_t left_a = (p.m - 1 - i0) * p.lda + p.k, left_b = (p.n - 1 - j0) * p.ldb + p.k;
+        const int64_t most = 0xfffffff0ll;
+        const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p.a + i0 * p.lda), 0,
+                                                          (int)(uint32_t)(((left_a < most ? left_a : most) + 15) & ~15ll), 0x00027000);
+        const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p.b + j0 * p.ldb), 0,
+                                                          (int)(uint32_t)(((left_b < most ? left_b : most) + 15) & ~15ll), 0x00027000);
+        // staging: a wave's instruction fills 8 rows; row r of 8, piece lane % 8
+        uint32_t at_a[4], at_b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = (j * 8 + wave) * 8 + (lane >> 3);
+            const int piece = (lane & 7) ^ (r & 7);
+            const int xa = r < rows_a ? r : rows_a - 1, xb = r < rows_b ? r : rows_b - 1;
+            at_a[j] = (uint32_t)xa * (uint32_t)p.lda + piece * 16;
+            at_b[j] = (uint32_t)xb * (uint32_t)p.ldb + piece * 16;
+        }
+        const auto load = [&](uint8_t *stage, int64_t g) {
+            typedef __attribute__((address_space(3))) void *lds_ptr;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(stage + (j * 8 + wave) * 1024), 16, at_a[j], (int)(g * kGroup), 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(stage + kBig * kGroup + (j * 8 + wave) * 1024), 16, at_b[j], (int)(g * kGroup), 0, 0);
+            }
+        };
+        const int32_t kb = (int32_t)p.kb;
+        ScaleWords sa{p.sa + i0 * kb, (int32_t)((p.m - i0) * kb - 4 < (1 << 30) ? (p.m - i0) * kb - 4 : (1 << 30))};
+        const int64_t sb_rows = ((p.n - 1) >> p.b_shift) + 1, sb0 = j0 >> p.b_shift;
+        ScaleWords sb{p.sb + sb0 * kb, (int32_t)((sb_rows - sb0) * kb - 4 < (1 << 30) ? (sb_rows - sb0) * kb - 4 : (1 << 30))};
+        int32_t sat[4], sbt[2];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int r = wm + x * 32 + row;
+            sat[x] = (r < rows_a ? r : rows_a - 1) * kb;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = wn + x * 32 + row;
+            sbt[x] = ((r < rows_b ? r : rows_b - 1) >> p.b_shift) * kb;
+        }
+        uint32_t ca[4], cb[2], na[4], nb[2];
+        const auto load_scales = [&](int32_t g) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                na[x] = scale_word(sa, sat[x] + g);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                nb[x] = scale_word(sb, sbt[x] + g);
+        };
+        f32x16 acc[2][4] = {};
+        const auto compute = [&](const uint8_t *stage) {
+            i32x8 fb[2][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = kBig + wn + x * 32 + row;
+                    fb[x][h] = operand(*reinterpret_cast<const u32x4 *>(stage + staged(r, h * 4 + half * 2)),
+                                       *reinterpret_cast<const u32x4 *>(stage + staged(r, h * 4 + half * 2 + 1)));
+                }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                i32x8 fa[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = wm + y * 32 + row;
+                    fa[h] = operand(*reinterpret_cast<const u32x4 *>(stage + staged(r, h * 4 + half * 2)),
+                                    *reinterpret_cast<const u32x4 *>(stage + staged(r, h * 4 + half * 2 + 1)));
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[x][h], fa[h], acc[x][y], ZR_E4M3, kFormatA, 0, (int)cb[x], 0, (int)ca[y]);
+            }
+        };
+        const auto step = [&](uint8_t *stage, uint8_t *next, int32_t g) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            if (g + 1 < kb)
+                load(next, g + 1);
+            if ((g & 3) == 0) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    ca[x] = na[x];
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    cb[x] = nb[x];
+                if (g + 4 < kb)
+                    load_scales(g + 4);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    ca[x] >>= 8;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    cb[x] >>= 8;
+            }
+            if (g + 1 == kb && p.k % kGroup) {  // zeros behind the last code of every row
+                const int tail = (int)(p.k % kGroup);
+                uint8_t *line = stage + t * kGroup;
+                for (int piece = tail / 16; piece < 8; ++piece) {
+                    u32x4 *w = reinterpret_cast<u32x4 *>(line + ((piece ^ (t & 7)) << 4));
+                    u32x4 v = *w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int keep = tail - piece * 16 - e * 4;  // bytes of the word that stay
+                        v[e] = keep >= 4 ? v[e] : keep <= 0 ? 0u : v[e] & ((1u << (8 * keep)) - 1u);
+                    }
+                    *w = v;
+                }
+                __syncthreads();
+            }
+            compute(stage);
+        };
+        __syncthreads();
+        load(stage0, 0);
+        load_scales(0);
+        for (int32_t g = 0; g < kb; g += 2) {
+            step(stage0, stage1, g);
+            if (g + 1 < kb)
+                step(stage1, stage0, g + 1);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int64_t i = i0 + wm + y * 32 + row;
+            if (i >= p.m)
+                continue;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t j = j0 + wn + x * 32 + e * 8 + half * 4;
+                    store_out(p, i, j, f32x4{acc[x][y][4 * e], acc[x][y][4 * e + 1], acc[x][y][4 * e + 2], acc[x][y][4 * e + 3]}, p.n - j);
+                }
+        }
+    }
+}
+
 namespace {
 
 template <int kFormatA, bool kWide>
 zr_status matmul_run(const MatmulArgs &p, hipStream_t st)
 {
+    if constexpr (!kWide) {
+        const bool aligned = aligned_to(p.a, 16) && aligned_to(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0 &&
+                             p.lda < (1 << 23) && p.ldb < (1 << 23) && p.m * p.kb >= 4 && (((p.n - 1) >> p.b_shift) + 1) * p.kb >= 4;
+        if (aligned && p.k > 0 && p.m > 256 && p.n >= 256) {
+            const int64_t bm = (p.m + kBig - 1) / kBig, bn = (p.n + kBig - 1) / kBig;
+            return launch(matmul_big_kernel<kFormatA>, grid_of(bm * bn), dim3(kBigThreads), 0, st, p, bm, bn);
+        }
+    }
     const int64_t tn = (p.n + kAnyTile - 1) / kAnyTile, tiles = tn * ((p.m + kAnyTile - 1) / kAnyTile);
     return launch(matmul_any_kernel<kFormatA, kWide>, grid_of(tiles), dim3(kBlock), 0, st, p, tn, tiles);
 }
