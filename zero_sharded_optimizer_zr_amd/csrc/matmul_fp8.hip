@@ -31,29 +31,81 @@ struct MatmulArgs {
     void *out;
     int64_t ldo;
     int32_t dtype, accumulate;
+    int32_t whole;  // rows of out start on 16-byte boundaries
 };
 
 constexpr int kAccum = 4;  // accumulators of a lane in a 16 x 16 tile
 
-// acc (column j .. j + 3 of row i) to out, the first `n` of them.
-__device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_t j, f32x4 acc, int64_t n)
+// Four (or eight) sums, columns j ... of row i, to out: the first `n` of them.
+template <typename T>
+__device__ __forceinline__ u32x2 add4(u32x2 old, f32x4 v, bool accumulate)
+{
+    if (accumulate)
+        v += f32x4{T::lo(old[0]), T::hi(old[0]), T::lo(old[1]), T::hi(old[1])};
+    return u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
+}
+
+__device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_t j, f32x4 v, int64_t n)
 {
     const int64_t at = i * p.ldo + j;
+    if (p.dtype == ZR_F32) {
+        float *o = static_cast<float *>(p.out) + at;
+        if (p.whole && n >= kAccum) {
+            const auto w = (global_ptr<f32x4>)o;
+            *w = p.accumulate ? *w + v : v;
+            return;
+        }
 #pragma unroll
-    for (int e = 0; e < kAccum; ++e) {
-        if (e >= n)
-            break;
-        if (p.dtype == ZR_F32) {
-            float *o = static_cast<float *>(p.out) + at + e;
-            *o = p.accumulate ? *o + acc[e] : acc[e];
+        for (int e = 0; e < kAccum; ++e)
+            if (e < n)
+                o[e] = p.accumulate ? o[e] + v[e] : v[e];
+        return;
+    }
+    uint16_t *o = static_cast<uint16_t *>(p.out) + at;
+    const bool vec = p.whole && n >= kAccum;
+    u32x2 w = {0, 0};
+    if (p.accumulate) {
+        if (vec) {
+            w = *(global_ptr<const u32x2>)o;
         } else {
-            uint16_t *o = static_cast<uint16_t *>(p.out) + at + e;
-            if (p.dtype == ZR_BF16)
-                *o = narrow<BF16>(p.accumulate ? widen<BF16>(*o) + acc[e] : acc[e]);
-            else
-                *o = narrow<F16>(p.accumulate ? widen<F16>(*o) + acc[e] : acc[e]);
+#pragma unroll
+            for (int e = 0; e < kAccum; ++e)
+                if (e < n)
+                    w[e / 2] |= (uint32_t)o[e] << (16 * (e % 2));
         }
     }
+    w = p.dtype == ZR_BF16 ? add4<BF16>(w, v, p.accumulate) : add4<F16>(w, v, p.accumulate);
+    if (vec) {
+        *(global_ptr<u32x2>)o = w;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < kAccum; ++e)
+        if (e < n)
+            o[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+}
+
+// The same for eight sums and a 16-bit out.
+__device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_t j, f32x4 lo, f32x4 hi, int64_t n)
+{
+    uint16_t *o = static_cast<uint16_t *>(p.out) + i * p.ldo + j;
+    u32x4 w = {0, 0, 0, 0};
+    if (p.accumulate)
+        w = p.whole ? load8<true>(o, n) : load8<false>(o, n);
+    const u32x2 a = {w[0], w[1]}, b = {w[2], w[3]};
+    u32x2 c, d;
+    if (p.dtype == ZR_BF16) {
+        c = add4<BF16>(a, lo, p.accumulate);
+        d = add4<BF16>(b, hi, p.accumulate);
+    } else {
+        c = add4<F16>(a, lo, p.accumulate);
+        d = add4<F16>(b, hi, p.accumulate);
+    }
+    w = u32x4{c[0], c[1], d[0], d[1]};
+    if (p.whole)
+        store8<true>(o, w, n);
+    else
+        store8<false>(o, w, n);
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -154,178 +206,259 @@ __global__ __launch_bounds__(kBlock) void matmul_any_kernel(MatmulArgs p, int64_
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kBig = 256;                  // output rows and columns of a workgroup
-constexpr int kBigThreads = 512;           // 8 waves: 2 down the rows x 4 across the columns
+constexpr int kCus = 256;                     // compute units: workgroups of a persistent launch
+constexpr int kBig = 256;                     // output rows and columns of a workgroup
 constexpr int kBigStage = 2 * kBig * kGroup;  // LDS bytes of one group of both operands
 
-__device__ __forceinline__ f32x16 multiply32(i32x8 b, int sb, i32x8 a, int sa, f32x16 acc)
+// Byte offset of 16-byte piece `piece` (of 8) of row `row` in a staged tile.
+__device__ __forceinline__ int staged(int row, int piece) { return row * kGroup + ((piece ^ (row >> 1 & 7)) << 4); }
+
+constexpr int kWaitAll = 0x0070;  // s_waitcnt vmcnt(0) lgkmcnt(0)
+
+// Sixteen bytes of each lane from `rsrc` at byte `at` + `k` into LDS from byte `to` on
+// (lane i at to + 16 i).  No register is written; the caller waits on vmcnt.  In
+// assembly because the compiler would wait for every such load before any read of
+// the same LDS array, also of the other stage.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t at, int k, uint32_t to)
 {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, ZR_E4M3, ZR_E4M3, 0, sb, 0, sa);
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(at), "s"(rsrc), "s"(k), "s"(to));
 }
 
-// Byte offset of 16-byte piece `piece` (of 8) of row `row` in a staged tile.
-__device__ __forceinline__ int staged(int row, int piece) { return row * kGroup + ((piece ^ (row & 7)) << 4); }
-
-struct ScaleWords {
-    const uint8_t *base;  // of the tile's first row
-    int32_t limit;        // last offset a word may be read at
+// One operand of the tile that is being loaded: `here` of its kBig rows exist, the
+// others are replaced by the last one (their results are dropped).
+struct BigOperand {
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t at[8];  // this lane's byte offsets in the 8 blocks of 32 rows
+    int32_t here;
+    uint32_t row0;   // row of the scales that the tile's first row has
 };
 
-// Four scale bytes from byte `at` on.
-__device__ __forceinline__ uint32_t scale_word(const ScaleWords &s, int32_t at)
+__device__ __forceinline__ BigOperand big_operand(const uint8_t *q, int64_t ld, int64_t rows, int64_t k, int64_t r0,
+                                                  int shift)
 {
-    const int32_t from = at < s.limit ? at : s.limit;
-    uint32_t w;
-    __builtin_memcpy(&w, s.base + from, 4);
-    return w >> (8 * (at - from));
+    const int t = threadIdx.x;
+    BigOperand o;
+    // up to the 16-byte piece that holds the last code
+    const int64_t left = ((rows - 1 - r0) * ld + k + 15) & ~15ll;
+    o.rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(q + r0 * ld), 0,
+                                               (int)(uint32_t)(left < 0xfffffff0ll ? left : 0xfffffff0ll), 0x00027000);
+    o.here = (int)(rows - r0 < kBig ? rows - r0 : kBig);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int r = j * 32 + (t >> 3);
+        uint32_t x = (uint32_t)(r < o.here ? r : o.here - 1) * (uint32_t)ld;
+        asm("" : "+v"(x));  // a 32-bit product
+        o.at[j] = x + (((t & 7) ^ (r >> 1 & 7)) << 4);
+    }
+    o.row0 = (uint32_t)(r0 >> shift);
+    return o;
+}
+
+// Four scale bytes from `at` on: read no further than `last`, the last offset at
+// which four may be read, and shifted into place where that moved the read.
+struct ScaleWord {
+    uint32_t word, shift;
+    __device__ __forceinline__ uint32_t get() const { return word >> shift; }
+};
+
+__device__ __forceinline__ ScaleWord scale_word(const uint8_t *scales, uint32_t last, uint32_t at)
+{
+    const uint32_t from = at < last ? at : last;
+    ScaleWord s;
+    __builtin_memcpy(&s.word, scales + from, 4);
+    s.shift = 8 * (at - from);
+    return s;
 }
 
 template <int kFormatA>
-__global__ __launch_bounds__(kBigThreads, 2) void matmul_big_kernel(MatmulArgs p, int64_t tiles_m, int64_t tiles_n)
+__global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int32_t tiles_m, int32_t tiles_n)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t stage0[kBigStage], stage1[kBigStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kBigStage];
+    __shared__ f32x4 turn[4][32 * 16];
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int wm = (wave >> 2) * 128, wn = (wave & 3) * 64, row = lane & 31, half = lane >> 5;
-    const int64_t tiles = tiles_m * tiles_n;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t tm = tile / tiles_n, tn = tile % tiles_n;
-        const int64_t i0 = tm * kBig, j0 = tn * kBig;
-        const int rows_a = (int)(p.m - i0 < kBig ? p.m - i0 : kBig), rows_b = (int)(p.n - j0 < kBig ? p.n - j0 : kBig);
-        const int64_t left_a = (p.m - 1 - i0) * p.lda + p.k, left_b = (p.n - 1 - j0) * p.ldb + p.k;
-        const int64_t most = 0xfffffff0ll;
-        const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p.a + i0 * p.lda), 0,
-                                                          (int)(uint32_t)(((left_a < most ? left_a : most) + 15) & ~15ll), 0x00027000);
-        const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p.b + j0 * p.ldb), 0,
-                                                          (int)(uint32_t)(((left_b < most ? left_b : most) + 15) & ~15ll), 0x00027000);
-        // staging: a wave's instruction fills 8 rows; row r of 8, piece lane % 8
-        uint32_t at_a[4], at_b[4];
+    const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128, row = lane & 31, half = lane >> 5;
+    const int32_t tiles = tiles_m * tiles_n;
+    const int32_t kb = (int32_t)p.kb;
+    const int tail = (int)(p.k % kGroup);
+    const uint32_t last_a = (uint32_t)(p.m * kb - 4), last_b = (uint32_t)((((p.n - 1) >> p.b_shift) + 1) * kb - 4);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+
+    const auto tile_at = [&](int32_t v, int64_t *i0, int64_t *j0) {
+        // one run of tiles per XCD; within it, strips of kStrip tile rows
+        constexpr int32_t kStrip = 8;
+        const int32_t x = v % kXcds, each = tiles / kXcds, more = tiles % kXcds;
+        const int32_t i = x * each + (x < more ? x : more) + v / kXcds;
+        const int32_t strip = i / (kStrip * tiles_n), r0 = strip * kStrip;
+        const int32_t high = tiles_m - r0 < kStrip ? tiles_m - r0 : kStrip;
+        const int32_t in = i - strip * kStrip * tiles_n;
+        *i0 = (int64_t)(r0 + in % high) * kBig;
+        *j0 = (int64_t)(in / high) * kBig;
+    };
+
+    // The loader: the tile and group that are loaded next, two groups ahead.  After
+    // the last tile it goes on with that tile's operands; nothing uses them.
+    int32_t load_tile = blockIdx.x;
+    int32_t load_g = 0;
+    BigOperand oa, ob;
+    ScaleWord na[4], nb[4];
+    const auto open_tile = [&]() {
+        int64_t i0, j0;
+        tile_at(load_tile, &i0, &j0);
+        oa = big_operand(p.a, p.lda, p.m, p.k, i0, 0);
+        ob = big_operand(p.b, p.ldb, p.n, p.k, j0, p.b_shift);
+    };
+    const auto load_piece = [&](int stage, int j) {
+        const uint32_t to = lds0 + stage + wave * 1024;
+        load_to_lds(oa.rsrc, oa.at[j], load_g * kGroup, to + j * 32 * kGroup);
+        load_to_lds(ob.rsrc, ob.at[j], load_g * kGroup, to + (kBig + j * 32) * kGroup);
+    };
+    const auto load_done = [&]() {
+        if ((load_g & 3) == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = (j * 8 + wave) * 8 + (lane >> 3);
-            const int piece = (lane & 7) ^ (r & 7);
-            const int xa = r < rows_a ? r : rows_a - 1, xb = r < rows_b ? r : rows_b - 1;
-            at_a[j] = (uint32_t)xa * (uint32_t)p.lda + piece * 16;
-            at_b[j] = (uint32_t)xb * (uint32_t)p.ldb + piece * 16;
-        }
-        const auto load = [&](uint8_t *stage, int64_t g) {
-            typedef __attribute__((address_space(3))) void *lds_ptr;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(stage + (j * 8 + wave) * 1024), 16, at_a[j], (int)(g * kGroup), 0, 0);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(stage + kBig * kGroup + (j * 8 + wave) * 1024), 16, at_b[j], (int)(g * kGroup), 0, 0);
+            for (int x = 0; x < 4; ++x) {
+                const int ra = wm + x * 32 + row, rb = wn + x * 32 + row;
+                na[x] = scale_word(p.sa, last_a, (oa.row0 + (uint32_t)(ra < oa.here ? ra : oa.here - 1)) * kb + load_g);
+                nb[x] = scale_word(p.sb, last_b, (ob.row0 + ((uint32_t)(rb < ob.here ? rb : ob.here - 1) >> p.b_shift)) * kb + load_g);
             }
-        };
-        const int32_t kb = (int32_t)p.kb;
-        ScaleWords sa{p.sa + i0 * kb, (int32_t)((p.m - i0) * kb - 4 < (1 << 30) ? (p.m - i0) * kb - 4 : (1 << 30))};
-        const int64_t sb_rows = ((p.n - 1) >> p.b_shift) + 1, sb0 = j0 >> p.b_shift;
-        ScaleWords sb{p.sb + sb0 * kb, (int32_t)((sb_rows - sb0) * kb - 4 < (1 << 30) ? (sb_rows - sb0) * kb - 4 : (1 << 30))};
-        int32_t sat[4], sbt[2];
+        }
+        if (++load_g == kb) {
+            load_g = 0;
+            load_tile += gridDim.x;
+            if (load_tile < tiles)
+                open_tile();
+        }
+    };
+    // zeros behind the last code of every row of a tile's last group
+    const auto clear_tail = [&](int stage) {
+        for (int r = t; r < 2 * kBig; r += kBlock)
+            for (int q = tail / 4; q < kGroup / 4; ++q) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(lds + stage + staged(r, q / 4) + q % 4 * 4);
+                *w = q == tail / 4 ? *w & ((1u << (8 * (tail % 4))) - 1u) : 0u;
+            }
+        __syncthreads();
+    };
+    const auto landed = [&]() {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(kWaitAll);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
+    i32x8 fa[2][4], fb[2][4];
+    uint32_t ca[4], cb[4];  // scales of the current group, in the low byte
+    f32x16 acc[4][4];
+    const auto read_one = [&](int stage, int h, int i) {  // i-th of 8 operands
+        const int x = i / 2, r = (i & 1 ? wm : kBig + wn) + x * 32 + row;
+        const i32x8 v = operand(*reinterpret_cast<const u32x4 *>(lds + stage + staged(r, h * 4 + half * 2)),
+                                *reinterpret_cast<const u32x4 *>(lds + stage + staged(r, h * 4 + half * 2 + 1)));
+        (i & 1 ? fa[h][x] : fb[h][x]) = v;
+    };
+    const auto multiply_one = [&](int h, int i) {
+        const int x = i & 3, y = i >> 2;
+        acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[h][x], fa[h][y], acc[x][y], ZR_E4M3, kFormatA,
+                                                                    0, (int)cb[x], 0, (int)ca[y]);
+        asm volatile("" : "+a"(acc[x][y]));  // here, not where the sum is next used
+    };
+    const auto take_words = [&](uint32_t *wa, uint32_t *wb) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const int r = wm + x * 32 + row;
-            sat[x] = (r < rows_a ? r : rows_a - 1) * kb;
+            wa[x] = na[x].get();
+            wb[x] = nb[x].get();
+            asm volatile("" : "+v"(wa[x]), "+v"(wb[x]));  // here, so that the next words need no other registers
         }
+    };
+    const auto clear_acc = [&]() {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int r = wn + x * 32 + row;
-            sbt[x] = ((r < rows_b ? r : rows_b - 1) >> p.b_shift) * kb;
-        }
-        uint32_t ca[4], cb[2], na[4], nb[2];
-        const auto load_scales = [&](int32_t g) {
+        for (int y = 0; y < 4; ++y)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                na[x] = scale_word(sa, sat[x] + g);
+                acc[x][y] = f32x16{};
+    };
+
+    f32x4 *const mine = turn[wave];
+    int32_t tile = blockIdx.x;
+    if (tile >= tiles)
+        return;
+    open_tile();
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-                nb[x] = scale_word(sb, sbt[x] + g);
-        };
-        f32x16 acc[2][4] = {};
-        const auto compute = [&](const uint8_t *stage) {
-            i32x8 fb[2][2];
+    for (int j = 0; j < 8; ++j)
+        load_piece(0, j);
+    load_done();
+    clear_acc();
+    landed();
+    take_words(ca, cb);
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+    for (int j = 0; j < 8; ++j)
+        load_piece(kBigStage, j);
+    load_done();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = kBig + wn + x * 32 + row;
-                    fb[x][h] = operand(*reinterpret_cast<const u32x4 *>(stage + staged(r, h * 4 + half * 2)),
-                                       *reinterpret_cast<const u32x4 *>(stage + staged(r, h * 4 + half * 2 + 1)));
-                }
+    for (int i = 0; i < 8; ++i)
+        read_one(0, 0, i);
+    int stage = 0;
+    for (;;) {
+        for (int32_t g = 0; g < kb; ++g) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                i32x8 fa[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = wm + y * 32 + row;
-                    fa[h] = operand(*reinterpret_cast<const u32x4 *>(stage + staged(r, h * 4 + half * 2)),
-                                    *reinterpret_cast<const u32x4 *>(stage + staged(r, h * 4 + half * 2 + 1)));
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[x][h], fa[h], acc[x][y], ZR_E4M3, kFormatA, 0, (int)cb[x], 0, (int)ca[y]);
+            for (int i = 0; i < 16; ++i) {
+                multiply_one(0, i);
+                if (i < 8)
+                    read_one(stage, 1, i);
+                __builtin_amdgcn_sched_barrier(0);
             }
-        };
-        const auto step = [&](uint8_t *stage, uint8_t *next, int32_t g) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            if (g + 1 < kb)
-                load(next, g + 1);
-            if ((g & 3) == 0) {
+            landed();  // the next group is in LDS, and this group's stage has been read by all
+            if (tail && g + 2 == kb)
+                clear_tail(stage ^ kBigStage);
+            uint32_t wa[4], wb[4];
+            take_words(wa, wb);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    ca[x] = na[x];
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    cb[x] = nb[x];
-                if (g + 4 < kb)
-                    load_scales(g + 4);
-            } else {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    ca[x] >>= 8;
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    cb[x] >>= 8;
+            for (int i = 0; i < 16; ++i) {
+                multiply_one(1, i);
+                if (i < 8) {
+                    load_piece(stage, i);
+                    read_one(stage ^ kBigStage, 0, i);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (g + 1 == kb && p.k % kGroup) {  // zeros behind the last code of every row
-                const int tail = (int)(p.k % kGroup);
-                uint8_t *line = stage + t * kGroup;
-                for (int piece = tail / 16; piece < 8; ++piece) {
-                    u32x4 *w = reinterpret_cast<u32x4 *>(line + ((piece ^ (t & 7)) << 4));
-                    u32x4 v = *w;
+            load_done();
+            const bool fresh = (g & 3) == 3 || g + 1 == kb;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int keep = tail - piece * 16 - e * 4;  // bytes of the word that stay
-                        v[e] = keep >= 4 ? v[e] : keep <= 0 ? 0u : v[e] & ((1u << (8 * keep)) - 1u);
+            for (int x = 0; x < 4; ++x) {
+                ca[x] = fresh ? wa[x] : ca[x] >> 8;
+                cb[x] = fresh ? wb[x] : cb[x] >> 8;
+            }
+            stage ^= kBigStage;
+        }
+        // Results: 32 rows x 64 columns at a time through the wave's own LDS (16-byte
+        // pieces, permuted by the row), so that 8 lanes store 128 bytes of a row.
+        int64_t i0, j0;
+        tile_at(tile, &i0, &j0);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int x = 0; x < 4; x += 2) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const f32x16 &v = acc[x + e / 4][y];
+                    const int q = e % 4, piece = e * 2 + half;  // columns 4 piece ... of the 64
+                    mine[row * 16 + (piece ^ (row & 15))] = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                }
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+                for (int r = lane >> 3; r < 32; r += 8) {
+                    const int piece = (lane & 7) * 2;
+                    const f32x4 lo = mine[r * 16 + (piece ^ (r & 15))], hi = mine[r * 16 + ((piece + 1) ^ (r & 15))];
+                    const int64_t i = i0 + wm + y * 32 + r, j = j0 + wn + x * 32 + piece * 4;
+                    if (i < p.m) {
+                        store_out(p, i, j, lo, hi, p.n - j);
                     }
-                    *w = v;
                 }
-                __syncthreads();
+                __builtin_amdgcn_wave_barrier();
             }
-            compute(stage);
-        };
-        __syncthreads();
-        load(stage0, 0);
-        load_scales(0);
-        for (int32_t g = 0; g < kb; g += 2) {
-            step(stage0, stage1, g);
-            if (g + 1 < kb)
-                step(stage1, stage0, g + 1);
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int64_t i = i0 + wm + y * 32 + row;
-            if (i >= p.m)
-                continue;
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int64_t j = j0 + wn + x * 32 + e * 8 + half * 4;
-                    store_out(p, i, j, f32x4{acc[x][y][4 * e], acc[x][y][4 * e + 1], acc[x][y][4 * e + 2], acc[x][y][4 * e + 3]}, p.n - j);
-                }
-        }
+        tile += gridDim.x;
+        __builtin_amdgcn_s_waitcnt(kWaitAll);  // also: no load into LDS outlives the workgroup
+        if (tile >= tiles)
+            break;
+        clear_acc();
     }
 }
 
@@ -337,9 +470,10 @@ zr_status matmul_run(const MatmulArgs &p, hipStream_t st)
     if constexpr (!kWide) {
         const bool aligned = aligned_to(p.a, 16) && aligned_to(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0 &&
                              p.lda < (1 << 23) && p.ldb < (1 << 23) && p.m * p.kb >= 4 && (((p.n - 1) >> p.b_shift) + 1) * p.kb >= 4;
-        if (aligned && p.k > 0 && p.m > 256 && p.n >= 256) {
+        if (aligned && p.kb > 1 && p.m > 256 && p.n >= 256) {
             const int64_t bm = (p.m + kBig - 1) / kBig, bn = (p.n + kBig - 1) / kBig;
-            return launch(matmul_big_kernel<kFormatA>, grid_of(bm * bn), dim3(kBigThreads), 0, st, p, bm, bn);
+            return launch(matmul_big_kernel<kFormatA>, grid_of(bm * bn < kCus ? bm * bn : kCus), dim3(kBlock), 0, st, p,
+                          (int32_t)bm, (int32_t)bn);
         }
     }
     const int64_t tn = (p.n + kAnyTile - 1) / kAnyTile, tiles = tn * ((p.m + kAnyTile - 1) / kAnyTile);
@@ -389,7 +523,7 @@ extern "C" zr_status zr_matmul_fp8(const uint8_t *a, int64_t lda, const uint8_t 
                 return fail(ZR_EINVAL, "%s: out overlaps another buffer", who);
     }
     const MatmulArgs p{a, b, a_scales, b_scales, lda, ldb, m, n, k, kb, b_block_rows == 1 ? 0 : 7, out, ldo,
-                       out_dtype, accumulate};
+                       out_dtype, accumulate, aligned_to(out, 16) && (ldo * size % 16 == 0 || m == 1)};
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (out_dtype == ZR_F32)
         return a_format == ZR_E4M3 ? matmul_run<ZR_E4M3, true>(p, st) : matmul_run<ZR_E5M2, true>(p, st);
