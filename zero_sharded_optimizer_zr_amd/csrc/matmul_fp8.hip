@@ -34,6 +34,10 @@ struct MatmulArgs {
     int32_t whole;  // rows of out start on 16-byte boundaries
 };
 
+constexpr int kWaitLoads = 0x0f70;   // s_waitcnt vmcnt(0)
+constexpr int kWaitAll = 0x0070;     // s_waitcnt vmcnt(0) lgkmcnt(0)
+constexpr int kWaitStage = 0x0071;   // s_waitcnt vmcnt(1) lgkmcnt(0)
+
 constexpr int kAccum = 4;  // accumulators of a lane in a 16 x 16 tile
 
 // Four (or eight) sums, columns j ... of row i, to out: the first `n` of them.
@@ -90,8 +94,12 @@ __device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_
 {
     uint16_t *o = static_cast<uint16_t *>(p.out) + i * p.ldo + j;
     u32x4 w = {0, 0, 0, 0};
-    if (p.accumulate)
+    if (p.accumulate) {
         w = p.whole ? load8<true>(o, n) : load8<false>(o, n);
+        // waited for here, where it is known that something was loaded: the compiler
+        // would wait again, for every load in flight, in the loop that follows
+        __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    }
     const u32x2 a = {w[0], w[1]}, b = {w[2], w[3]};
     u32x2 c, d;
     if (p.dtype == ZR_BF16) {
@@ -206,83 +214,87 @@ __global__ __launch_bounds__(kBlock) void matmul_any_kernel(MatmulArgs p, int64_
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kCus = 256;                     // compute units: workgroups of a persistent launch
-constexpr int kBig = 256;                     // output rows and columns of a workgroup
-constexpr int kBigStage = 2 * kBig * kGroup;  // LDS bytes of one group of both operands
+constexpr int kCus = 256;                    // compute units: workgroups of a persistent launch
+constexpr int kBig = 256;                    // output rows and columns of a workgroup
+constexpr int kOperandStage = kBig * kGroup;  // LDS bytes of one group of one operand
+constexpr int kStage = 2 * kOperandStage;
+constexpr int kScaleBlock = 4 * kBig * 4;     // LDS bytes of four groups' scales of both operands
 
-// Byte offset of 16-byte piece `piece` (of 8) of row `row` in a staged tile.
+// Byte offset of 16-byte piece `piece` (of 8) of row `row` in a staged operand: 16
+// rows' pieces of one column of pieces fall into all 64 banks.
 __device__ __forceinline__ int staged(int row, int piece) { return row * kGroup + ((piece ^ (row >> 1 & 7)) << 4); }
 
-constexpr int kWaitAll = 0x0070;  // s_waitcnt vmcnt(0) lgkmcnt(0)
-
-// Sixteen bytes of each lane from `rsrc` at byte `at` + `k` into LDS from byte `to` on
-// (lane i at to + 16 i).  No register is written; the caller waits on vmcnt.  In
+// 16 (or 4) bytes of each lane from `rsrc` at byte `at` + `k` into LDS from byte `to`
+// on, lane after lane.  No register is written; the caller waits on vmcnt.  In
 // assembly because the compiler would wait for every such load before any read of
-// the same LDS array, also of the other stage.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t at, int k, uint32_t to)
+// the same LDS array, also of another stage.
+__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t at, int k, uint32_t to)
 {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                  :: "v"(at), "s"(rsrc), "s"(k), "s"(to));
+}
+
+__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t at, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" :: "v"(at), "s"(rsrc), "s"(to));
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t *p, int64_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0,
+                                             (int)(uint32_t)(bytes < 0xfffffff0ll ? bytes : 0xfffffff0ll), 0x00027000);
 }
 
 // One operand of the tile that is being loaded: `here` of its kBig rows exist, the
 // others are replaced by the last one (their results are dropped).
 struct BigOperand {
     __amdgpu_buffer_rsrc_t rsrc;
-    uint32_t at[8];  // this lane's byte offsets in the 8 blocks of 32 rows
+    uint32_t at[8];  // this lane's byte offsets in the eight blocks of 32 rows
     int32_t here;
     uint32_t row0;   // row of the scales that the tile's first row has
 };
+
+// Byte offset of row r (or of the last one).
+__device__ __forceinline__ uint32_t row_at(int r, int here, int64_t ld)
+{
+    uint32_t x = (uint32_t)(r < here ? r : here - 1) * (uint32_t)ld;
+    asm("" : "+v"(x));  // a 32-bit product
+    return x;
+}
 
 __device__ __forceinline__ BigOperand big_operand(const uint8_t *q, int64_t ld, int64_t rows, int64_t k, int64_t r0,
                                                   int shift)
 {
     const int t = threadIdx.x;
     BigOperand o;
-    // up to the 16-byte piece that holds the last code
-    const int64_t left = ((rows - 1 - r0) * ld + k + 15) & ~15ll;
-    o.rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(q + r0 * ld), 0,
-                                               (int)(uint32_t)(left < 0xfffffff0ll ? left : 0xfffffff0ll), 0x00027000);
+    // up to the end of the 16-byte piece that holds the last code
+    o.rsrc = buffer(q + r0 * ld, ((rows - 1 - r0) * ld + k + 15) & ~15ll);
     o.here = (int)(rows - r0 < kBig ? rows - r0 : kBig);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int r = j * 32 + (t >> 3);
-        uint32_t x = (uint32_t)(r < o.here ? r : o.here - 1) * (uint32_t)ld;
-        asm("" : "+v"(x));  // a 32-bit product
-        o.at[j] = x + (((t & 7) ^ (r >> 1 & 7)) << 4);
+        o.at[j] = row_at(r, o.here, ld) + (((t & 7) ^ (r >> 1 & 7)) << 4);
     }
     o.row0 = (uint32_t)(r0 >> shift);
     return o;
 }
 
-// Four scale bytes from `at` on: read no further than `last`, the last offset at
-// which four may be read, and shifted into place where that moved the read.
-struct ScaleWord {
-    uint32_t word, shift;
-    __device__ __forceinline__ uint32_t get() const { return word >> shift; }
-};
-
-__device__ __forceinline__ ScaleWord scale_word(const uint8_t *scales, uint32_t last, uint32_t at)
-{
-    const uint32_t from = at < last ? at : last;
-    ScaleWord s;
-    __builtin_memcpy(&s.word, scales + from, 4);
-    s.shift = 8 * (at - from);
-    return s;
-}
-
 template <int kFormatA>
 __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int32_t tiles_m, int32_t tiles_n)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kBigStage];
-    __shared__ f32x4 turn[4][32 * 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+    __shared__ __attribute__((aligned(1024))) uint32_t words[2 * kScaleBlock / 4];
+    __shared__ uint32_t dump[64];  // what a prefetch brings; never read
+    __shared__ f32x4 turn[4][32 * 8];
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128, row = lane & 31, half = lane >> 5;
     const int32_t tiles = tiles_m * tiles_n;
     const int32_t kb = (int32_t)p.kb;
-    const int tail = (int)(p.k % kGroup);
-    const uint32_t last_a = (uint32_t)(p.m * kb - 4), last_b = (uint32_t)((((p.n - 1) >> p.b_shift) + 1) * kb - 4);
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+    const int tail = (int)(p.k % kGroup);  // codes of a last, short group
+    typedef __attribute__((address_space(3))) uint8_t *lds_address;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_address)lds;
+    const uint32_t dump0 = (uint32_t)(uintptr_t)(lds_address)reinterpret_cast<uint8_t *>(dump);
+    const uint32_t words0 = (uint32_t)(uintptr_t)(lds_address)reinterpret_cast<uint8_t *>(words);
 
     const auto tile_at = [&](int32_t v, int64_t *i0, int64_t *j0) {
         // one run of tiles per XCD; within it, strips of kStrip tile rows
@@ -296,31 +308,49 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
         *j0 = (int64_t)(in / high) * kBig;
     };
 
-    // The loader: the tile and group that are loaded next, two groups ahead.  After
-    // the last tile it goes on with that tile's operands; nothing uses them.
-    int32_t load_tile = blockIdx.x;
-    int32_t load_g = 0;
+    // Scales: aligned words that hold the bytes of four groups (of two words, where
+    // the bytes of a row start inside one), read no further than the word of the
+    // array's last byte.
+    const uint32_t low_a = (uint32_t)(uintptr_t)p.sa & 3, low_b = (uint32_t)(uintptr_t)p.sb & 3;
+    const uint32_t bytes_a = (uint32_t)(p.m * p.kb) + low_a;
+    const uint32_t bytes_b = (uint32_t)((((p.n - 1) >> p.b_shift) + 1) * p.kb) + low_b;
+    const auto rsa = buffer(p.sa - low_a, (bytes_a + 3) & ~3u), rsb = buffer(p.sb - low_b, (bytes_b + 3) & ~3u);
+    const bool split = (low_a | low_b | (p.kb & 3)) != 0;
+
+    // The loader: the tile and group that are loaded next, two groups ahead.  After the
+    // last tile it goes on with that tile's operands; nothing uses them.
+    int32_t load_tile = blockIdx.x, load_g = 0;
+    uint32_t load_words = 0;  // half of `words` that is filled next
     BigOperand oa, ob;
-    ScaleWord na[4], nb[4];
+    uint32_t ahead;           // this lane's row for prefetches
     const auto open_tile = [&]() {
         int64_t i0, j0;
         tile_at(load_tile, &i0, &j0);
         oa = big_operand(p.a, p.lda, p.m, p.k, i0, 0);
         ob = big_operand(p.b, p.ldb, p.n, p.k, j0, p.b_shift);
+        // a quarter of the rows of each operand: neighbouring tiles share the rest
+        const int quarter = (int)((wave < 2 ? j0 : i0) / kBig & 3) * 64 + (wave & 1) * 32 + lane;
+        ahead = lane < 32 ? row_at(quarter, wave < 2 ? oa.here : ob.here, wave < 2 ? p.lda : p.ldb) : 0xffffffffu;
     };
-    const auto load_piece = [&](int stage, int j) {
-        const uint32_t to = lds0 + stage + wave * 1024;
-        load_to_lds(oa.rsrc, oa.at[j], load_g * kGroup, to + j * 32 * kGroup);
-        load_to_lds(ob.rsrc, ob.at[j], load_g * kGroup, to + (kBig + j * 32) * kGroup);
+    const auto load_piece = [&](uint32_t stage, int j) {  // j-th of 16 pieces of this wave
+        const BigOperand &o = j & 1 ? oa : ob;
+        load16_to_lds(o.rsrc, o.at[j / 2], load_g * kGroup,
+                      lds0 + stage + (j & 1 ? 0 : kOperandStage) + j / 2 * 4096 + wave * 1024);
     };
     const auto load_done = [&]() {
-        if ((load_g & 3) == 0) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int ra = wm + x * 32 + row, rb = wn + x * 32 + row;
-                na[x] = scale_word(p.sa, last_a, (oa.row0 + (uint32_t)(ra < oa.here ? ra : oa.here - 1)) * kb + load_g);
-                nb[x] = scale_word(p.sb, last_b, (ob.row0 + ((uint32_t)(rb < ob.here ? rb : ob.here - 1) >> p.b_shift)) * kb + load_g);
+        if (load_g % 4 == 0) {
+            const uint32_t to = words0 + load_words + wave * 256, g = (uint32_t)load_g;
+            const uint32_t ra = oa.row0 + (uint32_t)(t < oa.here ? t : oa.here - 1);
+            const uint32_t rb = ob.row0 + ((uint32_t)(t < ob.here ? t : ob.here - 1) >> p.b_shift);
+            const uint32_t xa = (ra * (uint32_t)kb + g + low_a) & ~3u, xb = (rb * (uint32_t)kb + g + low_b) & ~3u;
+            load4_to_lds(rsa, xa, to);
+            load4_to_lds(rsb, xb, to + 2048);
+            if (split) {
+                const uint32_t last_a = (bytes_a - 1) & ~3u, last_b = (bytes_b - 1) & ~3u;
+                load4_to_lds(rsa, xa < last_a ? xa + 4 : last_a, to + 1024);
+                load4_to_lds(rsb, xb < last_b ? xb + 4 : last_b, to + 3072);
             }
+            load_words ^= kScaleBlock;
         }
         if (++load_g == kb) {
             load_g = 0;
@@ -329,43 +359,55 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
                 open_tile();
         }
     };
-    // zeros behind the last code of every row of a tile's last group
-    const auto clear_tail = [&](int stage) {
+    // Brings the lines of the group kAhead further on into the L2, where the loads of
+    // the XCD's workgroups, which run side by side, would all wait for them.
+    const auto prefetch = [&]() {
+        constexpr int32_t kAhead = 2;
+        const int32_t g = load_g + kAhead;
+        load4_to_lds(wave < 2 ? oa.rsrc : ob.rsrc, g < kb ? ahead + (uint32_t)g * kGroup : 0xffffffffu, dump0);
+    };
+    // zeros from code `tail` on in every row of a stage
+    const auto clear_tail = [&](uint32_t at) {
         for (int r = t; r < 2 * kBig; r += kBlock)
             for (int q = tail / 4; q < kGroup / 4; ++q) {
-                uint32_t *w = reinterpret_cast<uint32_t *>(lds + stage + staged(r, q / 4) + q % 4 * 4);
+                uint32_t *w = reinterpret_cast<uint32_t *>(lds + at + staged(r, q / 4) + q % 4 * 4);
                 *w = q == tail / 4 ? *w & ((1u << (8 * (tail % 4))) - 1u) : 0u;
             }
         __syncthreads();
-    };
-    const auto landed = [&]() {
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(kWaitAll);
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
     };
 
     i32x8 fa[2][4], fb[2][4];
     uint32_t ca[4], cb[4];  // scales of the current group, in the low byte
     f32x16 acc[4][4];
-    const auto read_one = [&](int stage, int h, int i) {  // i-th of 8 operands
+    const auto read_one = [&](uint32_t stage, int f, int i) {  // i-th of 8 operands
         const int x = i / 2, r = (i & 1 ? wm : kBig + wn) + x * 32 + row;
-        const i32x8 v = operand(*reinterpret_cast<const u32x4 *>(lds + stage + staged(r, h * 4 + half * 2)),
-                                *reinterpret_cast<const u32x4 *>(lds + stage + staged(r, h * 4 + half * 2 + 1)));
-        (i & 1 ? fa[h][x] : fb[h][x]) = v;
+        const i32x8 v = operand(*reinterpret_cast<const u32x4 *>(lds + stage + staged(r, f * 4 + half * 2)),
+                                *reinterpret_cast<const u32x4 *>(lds + stage + staged(r, f * 4 + half * 2 + 1)));
+        (i & 1 ? fa[f][x] : fb[f][x]) = v;
     };
-    const auto multiply_one = [&](int h, int i) {
+    const auto multiply_one = [&](int f, int i) {
         const int x = i & 3, y = i >> 2;
-        acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[h][x], fa[h][y], acc[x][y], ZR_E4M3, kFormatA,
+        acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[f][x], fa[f][y], acc[x][y], ZR_E4M3, kFormatA,
                                                                     0, (int)cb[x], 0, (int)ca[y]);
         asm volatile("" : "+a"(acc[x][y]));  // here, not where the sum is next used
     };
-    const auto take_words = [&](uint32_t *wa, uint32_t *wb) {
+    // The scales of four groups from `words`, for a tile whose first rows' scales are
+    // row_a and row_b.
+    const auto read_scales = [&](uint32_t from, uint32_t row_a, uint32_t row_b, uint32_t *wa, uint32_t *wb) {
+        const uint32_t *w = words + from / 4;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            wa[x] = na[x].get();
-            wb[x] = nb[x].get();
-            asm volatile("" : "+v"(wa[x]), "+v"(wb[x]));  // here, so that the next words need no other registers
+            wa[x] = w[wm + x * 32 + row];
+            wb[x] = w[512 + wn + x * 32 + row];
+        }
+        if (split) {  // rows 32 apart start at the same byte of a word
+            const uint32_t sa = (row_a + wm + row) * (uint32_t)kb + low_a;
+            const uint32_t sb = (row_b + ((wn + row) >> p.b_shift)) * (uint32_t)kb + low_b;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                wa[x] = __builtin_amdgcn_alignbyte(w[256 + wm + x * 32 + row], wa[x], sa);
+                wb[x] = __builtin_amdgcn_alignbyte(w[768 + wn + x * 32 + row], wb[x], sb);
+            }
         }
     };
     const auto clear_acc = [&]() {
@@ -382,22 +424,29 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
         return;
     open_tile();
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 16; ++j)
         load_piece(0, j);
     load_done();
     clear_acc();
-    landed();
-    take_words(ca, cb);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    uint32_t stage = 0, from = 0, row_a = oa.row0, row_b = ob.row0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        load_piece(kBigStage, j);
+    for (int j = 0; j < 16; ++j)
+        load_piece(kStage, j);
     load_done();
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         read_one(0, 0, i);
-    int stage = 0;
+    read_scales(from, row_a, row_b, ca, cb);
+    from ^= kScaleBlock;
     for (;;) {
         for (int32_t g = 0; g < kb; ++g) {
+            const bool last = g + 1 == kb;
+            // first half of the group, from registers; the second half's operands are read
+            prefetch();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 multiply_one(0, i);
@@ -405,61 +454,76 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
                     read_one(stage, 1, i);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            landed();  // the next group is in LDS, and this group's stage has been read by all
+            // the next group has landed (all but the prefetch), in every wave, and this
+            // group's stage has been read by all
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(kWaitStage);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
             if (tail && g + 2 == kb)
-                clear_tail(stage ^ kBigStage);
+                clear_tail(stage ^ kStage);
+            const bool fresh = last || (g & 3) == 3;
             uint32_t wa[4], wb[4];
-            take_words(wa, wb);
+            if (fresh) {  // of the next four groups, or of the next tile, which is already being loaded
+                row_a = last ? oa.row0 : row_a;
+                row_b = last ? ob.row0 : row_b;
+                read_scales(from, row_a, row_b, wa, wb);
+                from ^= kScaleBlock;
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    wa[x] = ca[x] >> 8;
+                    wb[x] = cb[x] >> 8;
+                }
+            }
+            // second half; the next group's first operands are read, and the group after
+            // it is loaded into this one's place
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 multiply_one(1, i);
-                if (i < 8) {
-                    load_piece(stage, i);
-                    read_one(stage ^ kBigStage, 0, i);
-                }
+                load_piece(stage, i);
+                if (i < 8)
+                    read_one(stage ^ kStage, 0, i);
                 __builtin_amdgcn_sched_barrier(0);
             }
             load_done();
-            const bool fresh = (g & 3) == 3 || g + 1 == kb;
+            stage ^= kStage;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                ca[x] = fresh ? wa[x] : ca[x] >> 8;
-                cb[x] = fresh ? wb[x] : cb[x] >> 8;
+                ca[x] = wa[x];
+                cb[x] = wb[x];
             }
-            stage ^= kBigStage;
         }
-        // Results: 32 rows x 64 columns at a time through the wave's own LDS (16-byte
-        // pieces, permuted by the row), so that 8 lanes store 128 bytes of a row.
+        // Results: 32 x 32 at a time through the wave's own LDS (16-byte pieces,
+        // permuted by the row), so that four lanes store 64 bytes of a row.
         int64_t i0, j0;
         tile_at(tile, &i0, &j0);
 #pragma unroll
         for (int y = 0; y < 4; ++y)
 #pragma unroll
-            for (int x = 0; x < 4; x += 2) {
+            for (int x = 0; x < 4; ++x) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const f32x16 &v = acc[x + e / 4][y];
-                    const int q = e % 4, piece = e * 2 + half;  // columns 4 piece ... of the 64
-                    mine[row * 16 + (piece ^ (row & 15))] = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                for (int q = 0; q < 4; ++q) {
+                    const f32x16 &v = acc[x][y];  // columns 8 q + 4 half ... of the 32
+                    mine[row * 8 + ((q * 2 + half) ^ (row & 7))] = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
                 }
                 __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-                for (int r = lane >> 3; r < 32; r += 8) {
-                    const int piece = (lane & 7) * 2;
-                    const f32x4 lo = mine[r * 16 + (piece ^ (r & 15))], hi = mine[r * 16 + ((piece + 1) ^ (r & 15))];
+                for (int r = lane >> 2; r < 32; r += 16) {
+                    const int piece = (lane & 3) * 2;
+                    const f32x4 lo = mine[r * 8 + (piece ^ (r & 7))], hi = mine[r * 8 + ((piece + 1) ^ (r & 7))];
                     const int64_t i = i0 + wm + y * 32 + r, j = j0 + wn + x * 32 + piece * 4;
-                    if (i < p.m) {
+                    if (i < p.m)
                         store_out(p, i, j, lo, hi, p.n - j);
-                    }
                 }
                 __builtin_amdgcn_wave_barrier();
             }
         tile += gridDim.x;
-        __builtin_amdgcn_s_waitcnt(kWaitAll);  // also: no load into LDS outlives the workgroup
         if (tile >= tiles)
             break;
         clear_acc();
     }
+    __builtin_amdgcn_s_waitcnt(kWaitAll);  // no load into LDS outlives the workgroup
 }
 
 namespace {
@@ -469,7 +533,7 @@ zr_status matmul_run(const MatmulArgs &p, hipStream_t st)
 {
     if constexpr (!kWide) {
         const bool aligned = aligned_to(p.a, 16) && aligned_to(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0 &&
-                             p.lda < (1 << 23) && p.ldb < (1 << 23) && p.m * p.kb >= 4 && (((p.n - 1) >> p.b_shift) + 1) * p.kb >= 4;
+                             p.lda < (1 << 23) && p.ldb < (1 << 23) && p.m * p.kb < (1ll << 31) && p.n * p.kb < (1ll << 31);
         if (aligned && p.kb > 1 && p.m > 256 && p.n >= 256) {
             const int64_t bm = (p.m + kBig - 1) / kBig, bn = (p.n + kBig - 1) / kBig;
             return launch(matmul_big_kernel<kFormatA>, grid_of(bm * bn < kCus ? bm * bn : kCus), dim3(kBlock), 0, st, p,
