@@ -34,6 +34,7 @@ struct MatmulArgs {
     int32_t whole;  // rows of out start on 16-byte boundaries
 };
 
+constexpr int kCus = 256;             // compute units
 constexpr int kWaitLoads = 0x0f70;   // s_waitcnt vmcnt(0)
 constexpr int kWaitAll = 0x0070;     // s_waitcnt vmcnt(0) lgkmcnt(0)
 constexpr int kWaitStage = 0x0071;   // s_waitcnt vmcnt(1) lgkmcnt(0)
@@ -49,24 +50,39 @@ __device__ __forceinline__ u32x2 add4(u32x2 old, f32x4 v, bool accumulate)
     return u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
 }
 
+// The old values of an accumulating product are waited for where they are loaded:
+// the compiler, which does not know there whether anything was, would wait again in
+// the loop that follows, for every load in flight.
 __device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_t j, f32x4 v, int64_t n)
 {
     const int64_t at = i * p.ldo + j;
+    const bool vec = p.whole && n >= kAccum;
     if (p.dtype == ZR_F32) {
         float *o = static_cast<float *>(p.out) + at;
-        if (p.whole && n >= kAccum) {
-            const auto w = (global_ptr<f32x4>)o;
-            *w = p.accumulate ? *w + v : v;
+        if (p.accumulate) {
+            f32x4 old = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (vec) {
+                old = *(global_ptr<const f32x4>)o;
+            } else {
+#pragma unroll
+                for (int e = 0; e < kAccum; ++e)
+                    if (e < n)
+                        old[e] = o[e];
+            }
+            __builtin_amdgcn_s_waitcnt(kWaitLoads);
+            v += old;
+        }
+        if (vec) {
+            *(global_ptr<f32x4>)o = v;
             return;
         }
 #pragma unroll
         for (int e = 0; e < kAccum; ++e)
             if (e < n)
-                o[e] = p.accumulate ? o[e] + v[e] : v[e];
+                o[e] = v[e];
         return;
     }
     uint16_t *o = static_cast<uint16_t *>(p.out) + at;
-    const bool vec = p.whole && n >= kAccum;
     u32x2 w = {0, 0};
     if (p.accumulate) {
         if (vec) {
@@ -77,6 +93,7 @@ __device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_
                 if (e < n)
                     w[e / 2] |= (uint32_t)o[e] << (16 * (e % 2));
         }
+        __builtin_amdgcn_s_waitcnt(kWaitLoads);
     }
     w = p.dtype == ZR_BF16 ? add4<BF16>(w, v, p.accumulate) : add4<F16>(w, v, p.accumulate);
     if (vec) {
@@ -96,8 +113,6 @@ __device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_
     u32x4 w = {0, 0, 0, 0};
     if (p.accumulate) {
         w = p.whole ? load8<true>(o, n) : load8<false>(o, n);
-        // waited for here, where it is known that something was loaded: the compiler
-        // would wait again, for every load in flight, in the loop that follows
         __builtin_amdgcn_s_waitcnt(kWaitLoads);
     }
     const u32x2 a = {w[0], w[1]}, b = {w[2], w[3]};
@@ -121,12 +136,12 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // Eight codes times a power of two, as bf16.
 template <int kFormat>
-__device__ __forceinline__ bf16x8 widen8(int lo, int hi, float scale)
+__device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi, float scale)
 {
     bf16x8 o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int w = i < 2 ? lo : hi;
+        const int w = (int)(i < 2 ? lo : hi);
         bf16x2 p;
         if constexpr (kFormat == ZR_E4M3)
             p = i % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true)
@@ -140,72 +155,215 @@ __device__ __forceinline__ bf16x8 widen8(int lo, int hi, float scale)
     return o;
 }
 
-// A lane's 32 codes of a 16 x 128 operand from two 16-byte pieces.
+// A lane's 32 codes of an operand from two 16-byte pieces.
 __device__ __forceinline__ i32x8 operand(u32x4 lo, u32x4 hi)
 {
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-__device__ __forceinline__ i32x8 operand_at(const uint8_t *p)
+// ------------------------------------------ few rows, fp32 outputs, any alignment --
+
+// A wave computes 16 MT x 16 NT outputs over a range of groups, its operands loaded
+// straight into registers (a lane's 32 codes of a group are pieces `quad` and `quad`
+// + 4 of its row: 16 rows x 64 bytes an instruction), `kAhead` groups ahead of their
+// use.  kSplit waves of a workgroup share a tile and a kSplit-th of the groups each;
+// their sums meet in LDS and are added in wave order.  So a product with few
+// tiles still occupies the chip, without a workspace.
+constexpr int kSplitThreads = 512;
+constexpr int kSplitWaves = kSplitThreads / 64;
+
+// 16 codes at `p`, of which `n` belong to the row; the others count as zeros.
+// Nothing behind the row is read.
+__device__ __forceinline__ u32x4 codes16(const uint8_t *p, int n)
 {
-    return operand(*reinterpret_cast<const u32x4 *>(p), *reinterpret_cast<const u32x4 *>(p + 16));
+    u32x4 w = {0, 0, 0, 0};
+    if (n >= 16) {
+        __builtin_memcpy(&w, (global_ptr<const uint8_t>)p, 16);
+    } else {
+#pragma unroll 1
+        for (int e = 0; e < n; ++e) {
+            const uint32_t byte = (uint32_t)load_global(p + e) << (8 * (e % 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] |= e / 4 == i ? byte : 0u;
+        }
+    }
+    return w;
 }
 
-// acc += B's 16 rows times A's 16 rows over one group of 128: codes fb and fa (any
-// order of the 128 in which both agree), scale bytes sb and sa in the low byte.
-template <int kFormatA, bool kWide>
-__device__ __forceinline__ f32x4 multiply(i32x8 fb, int sb, i32x8 fa, int sa, f32x4 acc)
+// Each of the four rows of 16 lanes, spread over all four.
+__device__ __forceinline__ void spread_quads(uint32_t v, uint32_t *out)
 {
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    out[0] = lo[0];
+    out[1] = lo[1];
+    out[2] = hi[0];
+    out[3] = hi[1];
+}
+
+// One group's operands and scales of a wave's tile.
+template <int MT, int NT>
+struct SplitGroup {
+    u32x4 a[MT][2], b[NT][2];
+    uint32_t sa, sb;  // of row 16 quad + lane % 16
+};
+
+// acc += the products of one group.
+template <int kFormatA, bool kWide, int MT, int NT>
+__device__ __forceinline__ void multiply_group(const SplitGroup<MT, NT> &s, f32x4 (&acc)[MT][NT])
+{
+    uint32_t ca[4], cb[4];
+    spread_quads(s.sa, ca);
+    spread_quads(s.sb, cb);
     if constexpr (!kWide) {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc, ZR_E4M3, kFormatA, 0, sb, 0, sa);
-    } else {
-        const float xb = __uint_as_float((uint32_t)sb << 23), xa = __uint_as_float((uint32_t)sa << 23);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<ZR_E4M3>(fb[2 * i], fb[2 * i + 1], xb),
-                                                          widen8<kFormatA>(fa[2 * i], fa[2 * i + 1], xa), acc, 0, 0, 0);
-        return acc;
+        for (int y = 0; y < MT; ++y)
+#pragma unroll
+            for (int z = 0; z < NT; ++z)
+                acc[y][z] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    operand(s.b[z][0], s.b[z][1]), operand(s.a[y][0], s.a[y][1]), acc[y][z], ZR_E4M3, kFormatA, 0,
+                    (int)cb[z], 0, (int)ca[y]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 8 codes of each lane at a time
+            const int h = i / 2, e = i % 2 * 2;
+            bf16x8 b[NT];
+#pragma unroll
+            for (int z = 0; z < NT; ++z)
+                b[z] = widen8<ZR_E4M3>(s.b[z][h][e], s.b[z][h][e + 1], __uint_as_float(cb[z] << 23));
+#pragma unroll
+            for (int y = 0; y < MT; ++y) {
+                const bf16x8 a = widen8<kFormatA>(s.a[y][h][e], s.a[y][h][e + 1], __uint_as_float(ca[y] << 23));
+#pragma unroll
+                for (int z = 0; z < NT; ++z)
+                    acc[y][z] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[z], a, acc[y][z], 0, 0, 0);
+            }
+        }
     }
 }
 
-// Any alignment and any sizes: a workgroup computes 64 x 64 outputs, its codes
-// staged through LDS byte by byte with zeros outside the matrices.
-constexpr int kAnyTile = 64;
-constexpr int kAnyRow = kGroup + 16;  // LDS bytes of a staged row
-
-template <int kFormatA, bool kWide>
-__global__ __launch_bounds__(kBlock) void matmul_any_kernel(MatmulArgs p, int64_t tiles_n, int64_t tiles)
+template <int kFormatA, bool kWide, int MT, int NT, int kAhead>
+__global__ __launch_bounds__(kSplitThreads, 2) void matmul_split_kernel(MatmulArgs p, int32_t split, int64_t tiles_m,
+                                                                        int64_t rounds)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t la[kAnyTile * kAnyRow], lb[kAnyTile * kAnyRow];
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, row = lane & 15, quad = lane >> 4;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t i0 = tile / tiles_n * kAnyTile, j0 = tile % tiles_n * kAnyTile;
-        f32x4 acc[4] = {};
-        for (int64_t g = 0; g < p.kb; ++g) {
-            __syncthreads();
-            for (int e = t; e < kAnyTile * kGroup; e += kBlock) {
-                const int r = e / kGroup, c = e % kGroup;
-                const int64_t kk = g * kGroup + c;
-                la[r * kAnyRow + c] = i0 + r < p.m && kk < p.k ? p.a[(i0 + r) * p.lda + kk] : 0;
-                lb[r * kAnyRow + c] = j0 + r < p.n && kk < p.k ? p.b[(j0 + r) * p.ldb + kk] : 0;
-            }
-            __syncthreads();
-            const int64_t j = j0 + wave * 16 + row;
-            const int sb = j < p.n ? p.sb[(j >> p.b_shift) * p.kb + g] : 0;
-            const i32x8 fb = operand_at(lb + (wave * 16 + row) * kAnyRow + quad * 32);
+    __shared__ f32x4 part[kSplitWaves][MT * NT][64];
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int row = lane & 15, quad = lane >> 4;
+    const int share = wave % split, slot = wave / split, slots = kSplitWaves / split;
+    const int32_t kb = (int32_t)p.kb, whole = (int32_t)(p.k / kGroup);
+    const int64_t tiles_n = (p.n + 16 * NT - 1) / (16 * NT), tiles = tiles_m * tiles_n;
+    for (int64_t round = blockIdx.x; round < rounds; round += gridDim.x) {
+        // one run of rounds per XCD; neighbouring tiles share their rows of B
+        const int64_t x = round % kXcds, each = rounds / kXcds, more = rounds % kXcds;
+        const int64_t tile = (x * each + (x < more ? x : more) + round / kXcds) * slots + slot;
+        const bool live = tile < tiles;
+        const int64_t i0 = live ? tile % tiles_m * (16 * MT) : 0, j0 = live ? tile / tiles_m * (16 * NT) : 0;
+        const uint8_t *pa[MT], *pb[NT];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int64_t i = i0 + x * 16 + row;
-                const int sa = i < p.m ? p.sa[i * p.kb + g] : 0;
-                const i32x8 fa = operand_at(la + (x * 16 + row) * kAnyRow + quad * 32);
-                acc[x] = multiply<kFormatA, kWide>(fb, sb, fa, sa, acc[x]);
-            }
+        for (int y = 0; y < MT; ++y) {
+            const int64_t i = i0 + y * 16 + row;
+            pa[y] = p.a + (i < p.m ? i : p.m - 1) * p.lda + quad * 16;
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int64_t i = i0 + x * 16 + row, j = j0 + wave * 16 + quad * 4;
+        for (int z = 0; z < NT; ++z) {
+            const int64_t j = j0 + z * 16 + row;
+            pb[z] = p.b + (j < p.n ? j : p.n - 1) * p.ldb + quad * 16;
+        }
+        const int64_t ia = i0 + lane, jb = j0 + lane;
+        const uint8_t *psa = p.sa + (ia < p.m ? ia : p.m - 1) * kb;
+        const uint8_t *psb = p.sb + ((jb < p.n ? jb : p.n - 1) >> p.b_shift) * kb;
+        f32x4 acc[MT][NT] = {};
+        // loads the group at the pointers and moves them on
+        const auto load = [&](SplitGroup<MT, NT> &s) {
+#pragma unroll
+            for (int z = 0; z < NT; ++z) {
+                __builtin_memcpy(&s.b[z][0], (global_ptr<const uint8_t>)pb[z], 16);
+                __builtin_memcpy(&s.b[z][1], (global_ptr<const uint8_t>)pb[z] + 64, 16);
+                pb[z] += kGroup;
+            }
+#pragma unroll
+            for (int y = 0; y < MT; ++y) {
+                __builtin_memcpy(&s.a[y][0], (global_ptr<const uint8_t>)pa[y], 16);
+                __builtin_memcpy(&s.a[y][1], (global_ptr<const uint8_t>)pa[y] + 64, 16);
+                pa[y] += kGroup;
+            }
+            s.sa = load_global(psa++);
+            s.sb = load_global(psb++);
+        };
+        // this wave's share of the whole groups
+        const int32_t first = (int32_t)((int64_t)whole * share / split), end = (int32_t)((int64_t)whole * (share + 1) / split);
+#pragma unroll
+        for (int y = 0; y < MT; ++y)
+            pa[y] += (int64_t)first * kGroup;
+#pragma unroll
+        for (int z = 0; z < NT; ++z)
+            pb[z] += (int64_t)first * kGroup;
+        psa += first;
+        psb += first;
+        if (live) {
+            SplitGroup<MT, NT> s[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (first + u < end)
+                    load(s[u]);
+            for (int32_t g = first; g < end; g += kAhead)
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    if (g + u < end)
+                        multiply_group<kFormatA, kWide>(s[u], acc);
+                    if (g + u + kAhead < end)
+                        load(s[u]);
+                }
+            if (whole < kb && share == split - 1) {  // the short last group
+                const int left = (int)(p.k - (int64_t)whole * kGroup) - quad * 16;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int z = 0; z < NT; ++z)
+                        s[0].b[z][h] = codes16(pb[z] + h * 64, left - h * 64);
+#pragma unroll
+                    for (int y = 0; y < MT; ++y)
+                        s[0].a[y][h] = codes16(pa[y] + h * 64, left - h * 64);
+                }
+                s[0].sa = load_global(psa);
+                s[0].sb = load_global(psb);
+                multiply_group<kFormatA, kWide>(s[0], acc);
+            }
+        }
+        if (split == 1) {
+            if (live) {
+#pragma unroll
+                for (int y = 0; y < MT; ++y)
+#pragma unroll
+                    for (int z = 0; z < NT; ++z) {
+                        const int64_t i = i0 + y * 16 + row, j = j0 + z * 16 + quad * 4;
+                        if (i < p.m)
+                            store_out(p, i, j, acc[y][z], p.n - j);
+                    }
+            }
+            continue;
+        }
+        __syncthreads();  // the last round's sums have been read
+#pragma unroll
+        for (int y = 0; y < MT; ++y)
+#pragma unroll
+            for (int z = 0; z < NT; ++z)
+                part[wave][y * NT + z][lane] = acc[y][z];
+        __syncthreads();
+        for (int c = wave; c < slots * MT * NT; c += kSplitWaves) {
+            const int sl = c / (MT * NT), yz = c % (MT * NT);
+            const int64_t other = tile - slot + sl;
+            if (other >= tiles)
+                break;
+            f32x4 sum = part[sl * split][yz][lane];
+            for (int w = 1; w < split; ++w)
+                sum += part[sl * split + w][yz][lane];
+            const int64_t i = other % tiles_m * (16 * MT) + yz / NT * 16 + row;
+            const int64_t j = other / tiles_m * (16 * NT) + yz % NT * 16 + quad * 4;
             if (i < p.m)
-                store_out(p, i, j, acc[x], p.n - j);
+                store_out(p, i, j, sum, p.n - j);
         }
     }
 }
@@ -214,7 +372,6 @@ __global__ __launch_bounds__(kBlock) void matmul_any_kernel(MatmulArgs p, int64_
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kCus = 256;                    // compute units: workgroups of a persistent launch
 constexpr int kBig = 256;                    // output rows and columns of a workgroup
 constexpr int kOperandStage = kBig * kGroup;  // LDS bytes of one group of one operand
 constexpr int kStage = 2 * kOperandStage;
@@ -298,7 +455,7 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
 
     const auto tile_at = [&](int32_t v, int64_t *i0, int64_t *j0) {
         // one run of tiles per XCD; within it, strips of kStrip tile rows
-        constexpr int32_t kStrip = 8;
+        constexpr int32_t kStrip = 4;
         const int32_t x = v % kXcds, each = tiles / kXcds, more = tiles % kXcds;
         const int32_t i = x * each + (x < more ? x : more) + v / kXcds;
         const int32_t strip = i / (kStrip * tiles_n), r0 = strip * kStrip;
@@ -362,7 +519,7 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
     // Brings the lines of the group kAhead further on into the L2, where the loads of
     // the XCD's workgroups, which run side by side, would all wait for them.
     const auto prefetch = [&]() {
-        constexpr int32_t kAhead = 2;
+        constexpr int32_t kAhead = 1;
         const int32_t g = load_g + kAhead;
         load4_to_lds(wave < 2 ? oa.rsrc : ob.rsrc, g < kb ? ahead + (uint32_t)g * kGroup : 0xffffffffu, dump0);
     };
@@ -526,22 +683,279 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
     __builtin_amdgcn_s_waitcnt(kWaitAll);  // no load into LDS outlives the workgroup
 }
 
+// ------------------------------------------------------------ middling products --
+
+// A workgroup computes 128 x 128 outputs, a wave 64 x 64, through a ring of kRing
+// groups of both operands in LDS, with the operands of the next group read into
+// registers while one is multiplied.  For products with too few 256 x 256 tiles to
+// occupy the chip, and for fp32 outputs.
+constexpr int kMid = 128;
+constexpr int kRing = 4;
+constexpr int kMidOperand = kMid * kGroup;
+constexpr int kMidStage = 2 * kMidOperand;
+constexpr int kMidWords = 2 * kMid * 16;      // LDS bytes of eight groups' scales of both operands
+constexpr int kMidWordRing = 8;               // more than the blocks of eight (or fewer) groups in use at once
+constexpr int kWaitRing = 0x4070;             // s_waitcnt vmcnt(16) lgkmcnt(0): all but two stages
+
+template <int kFormatA, bool kWide>
+__global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int32_t tiles_m, int32_t tiles_n)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing * kMidStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t words[kMidWordRing * kMidWords];
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64, row = lane & 15, quad = lane >> 4;
+    const int32_t tiles = tiles_m * tiles_n, kb = (int32_t)p.kb;
+    const int tail = (int)(p.k % kGroup);
+    typedef __attribute__((address_space(3))) uint8_t *lds_address;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_address)lds, words0 = (uint32_t)(uintptr_t)(lds_address)words;
+
+    // one run of tiles per XCD, down the columns of tiles: they share their rows of B
+    const auto tile_at = [&](int32_t v, int64_t *i0, int64_t *j0) {
+        const int32_t x = v % kXcds, each = tiles / kXcds, more = tiles % kXcds;
+        const int32_t i = x * each + (x < more ? x : more) + v / kXcds;
+        *i0 = (int64_t)(i % tiles_m) * kMid;
+        *j0 = (int64_t)(i / tiles_m) * kMid;
+    };
+
+    // Scales: the 16 bytes from the word on that holds a row's first byte of eight
+    // groups; words behind the array's last one read as zeros.
+    const uint32_t low_a = (uint32_t)(uintptr_t)p.sa & 3, low_b = (uint32_t)(uintptr_t)p.sb & 3;
+    const auto rsa = buffer(p.sa - low_a, (p.m * kb + low_a + 3) & ~3ll);
+    const auto rsb = buffer(p.sb - low_b, ((((p.n - 1) >> p.b_shift) + 1) * kb + low_b + 3) & ~3ll);
+
+    // The loader, kRing groups ahead; after the last tile it goes on with that tile's
+    // operands, which nothing uses.
+    int32_t load_tile = blockIdx.x, load_g = 0;
+    uint32_t load_words = 0;
+    __amdgpu_buffer_rsrc_t ra, rb;
+    uint32_t at_a[4], at_b[4], at_s;
+    const auto open_tile = [&]() {
+        int64_t i0, j0;
+        tile_at(load_tile, &i0, &j0);
+        ra = buffer(p.a + i0 * p.lda, ((p.m - 1 - i0) * p.lda + p.k + 15) & ~15ll);
+        rb = buffer(p.b + j0 * p.ldb, ((p.n - 1 - j0) * p.ldb + p.k + 15) & ~15ll);
+        const int here_a = (int)(p.m - i0 < kMid ? p.m - i0 : kMid), here_b = (int)(p.n - j0 < kMid ? p.n - j0 : kMid);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = j * 32 + (t >> 3);
+            const uint32_t piece = (uint32_t)((t & 7) ^ (r >> 1 & 7)) << 4;
+            at_a[j] = row_at(r, here_a, p.lda) + piece;
+            at_b[j] = row_at(r, here_b, p.ldb) + piece;
+        }
+        // waves 0 and 1 bring A's scales, waves 2 and 3 B's
+        const int r = t & 127;
+        const uint32_t sr = wave < 2 ? (uint32_t)i0 + (uint32_t)(r < here_a ? r : here_a - 1)
+                                     : (uint32_t)(j0 + (r < here_b ? r : here_b - 1)) >> p.b_shift;
+        at_s = sr * (uint32_t)kb + (wave < 2 ? low_a : low_b);
+    };
+    const auto load_piece = [&](uint32_t stage, int j) {  // j-th of 8 pieces of this wave
+        load16_to_lds(j & 1 ? ra : rb, j & 1 ? at_a[j / 2] : at_b[j / 2], load_g * kGroup,
+                      lds0 + stage + (j & 1 ? 0 : kMidOperand) + j / 2 * 4096 + wave * 1024);
+    };
+    const auto load_done = [&]() {
+        if (load_g % 8 == 0) {
+            load16_to_lds(wave < 2 ? rsa : rsb, (at_s + (uint32_t)load_g) & ~3u, 0, words0 + load_words + wave * 1024);
+            load_words = load_words == (kMidWordRing - 1) * kMidWords ? 0 : load_words + kMidWords;
+        }
+        if (++load_g == kb) {
+            load_g = 0;
+            load_tile += gridDim.x;
+            if (load_tile < tiles)
+                open_tile();
+        }
+    };
+    const auto clear_tail = [&](uint32_t at) {
+        for (int q = tail / 4; q < kGroup / 4; ++q) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(lds + at + staged(t, q / 4) + q % 4 * 4);
+            *w = q == tail / 4 ? *w & ((1u << (8 * (tail % 4))) - 1u) : 0u;
+        }
+        __syncthreads();
+    };
+
+    SplitGroup<4, 4> f[2];
+    uint32_t ca[2][4], cb[2][4];
+    f32x4 acc[4][4];
+    // i-th of 16 reads of the operands of the group at `stage`
+    const auto read_one = [&](uint32_t stage, int e, int i) {
+        const int x = i >> 2, piece = quad + (i >> 1 & 1) * 4;
+        if (i & 1)
+            f[e].a[x][i >> 1 & 1] = *reinterpret_cast<const u32x4 *>(lds + stage + staged(wm + x * 16 + row, piece));
+        else
+            f[e].b[x][i >> 1 & 1] = *reinterpret_cast<const u32x4 *>(lds + stage + staged(kMid + wn + x * 16 + row, piece));
+    };
+    // the scales of the next group: its place in `words` and this lane's bytes in it
+    uint32_t word = 0, first_a = 0, first_b = 0;
+    const auto first_bytes = [&](int64_t i0, int64_t j0) {  // rows 16 apart start at the same byte of a word
+        const int64_t ia = i0 + wm + row, jb = j0 + wn + row;
+        first_a = (uint32_t)(wm + row) * 16 + (((uint32_t)ia * (uint32_t)kb + low_a) & 3);
+        first_b = (uint32_t)(kMid + wn + row) * 16 + (((uint32_t)(jb >> p.b_shift) * (uint32_t)kb + low_b) & 3);
+    };
+    const auto read_scale = [&](int e, int i, int32_t g) {  // i-th of 8
+        const uint8_t *w = words + word + (g & 7) + i / 2 * 256;
+        (i & 1 ? ca : cb)[e][i / 2] = w[i & 1 ? first_a : first_b];
+    };
+    const auto clear_acc = [&]() {
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                acc[y][z] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+
+    int32_t tile = blockIdx.x;
+    if (tile >= tiles)
+        return;
+    open_tile();
+#pragma unroll
+    for (int s = 0; s < kRing; ++s) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            load_piece(s * kMidStage, j);
+        load_done();
+    }
+    clear_acc();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (tail && kb == 1)
+        clear_tail(0);
+    if (tail && kb <= 2)
+        clear_tail(kMidStage);
+    int64_t i0, j0;
+    tile_at(tile, &i0, &j0);
+    first_bytes(i0, j0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        read_one(0, 0, i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        read_scale(0, i, 0);
+    uint32_t stage = 0;
+    int32_t g = 0, two = 2 % kb;  // the group that is multiplied, and the one two stages on
+
+    // Group g is multiplied from registers e while the next group's operands are read
+    // into the other ones and the group kRing on is loaded into g's place.
+    const auto step = [&](int e) {
+        const uint32_t next = (stage + kMidStage) % (kRing * kMidStage);
+        const bool last = g + 1 == kb;
+        const int32_t gn = last ? 0 : g + 1;
+        if (gn % 8 == 0) {
+            word = word == (kMidWordRing - 1) * kMidWords ? 0 : word + kMidWords;
+            if (last && tile + (int32_t)gridDim.x < tiles) {
+                tile_at(tile + gridDim.x, &i0, &j0);
+                first_bytes(i0, j0);
+            }
+        }
+        bf16x8 b[4], a;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if constexpr (!kWide) {
+                const int y = i >> 2, z = i & 3;
+                acc[y][z] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    operand(f[e].b[z][0], f[e].b[z][1]), operand(f[e].a[y][0], f[e].a[y][1]), acc[y][z], ZR_E4M3,
+                    kFormatA, 0, (int)cb[e][z], 0, (int)ca[e][y]);
+                asm volatile("" : "+v"(acc[y][z]));
+            } else {  // 8 codes of each lane, one row of tiles
+                const int q = i >> 2, y = i & 3, h = q / 2, c = q % 2 * 2;
+                if (y == 0)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        b[z] = widen8<ZR_E4M3>(f[e].b[z][h][c], f[e].b[z][h][c + 1], __uint_as_float(cb[e][z] << 23));
+                a = widen8<kFormatA>(f[e].a[y][h][c], f[e].a[y][h][c + 1], __uint_as_float(ca[e][y] << 23));
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    acc[y][z] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[z], a, acc[y][z], 0, 0, 0);
+                    asm volatile("" : "+v"(acc[y][z]));
+                }
+            }
+            read_one(next, e ^ 1, i);
+            if (i & 1)
+                load_piece(stage, i / 2);
+            else
+                read_scale(e ^ 1, i / 2, gn);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        load_done();
+        // two stages on has landed, in every wave, and the next one has been read by all
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(kWaitRing);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (tail && two + 1 == kb)
+            clear_tail((stage + 2 * kMidStage) % (kRing * kMidStage));
+        two = two + 1 == kb ? 0 : two + 1;
+        stage = next;
+        g = gn;
+    };
+    // Stores a finished tile; false after the last one.
+    int64_t out_i, out_j;
+    tile_at(tile, &out_i, &out_j);
+    const auto finish = [&]() {
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const int64_t i = out_i + wm + y * 16 + row, j = out_j + wn + z * 16 + quad * 4;
+                if (i < p.m)
+                    store_out(p, i, j, acc[y][z], p.n - j);
+            }
+        tile += gridDim.x;
+        if (tile >= tiles)
+            return false;
+        out_i = i0;
+        out_j = j0;
+        clear_acc();
+        return true;
+    };
+    for (;;) {
+        step(0);
+        if (g == 0 && !finish())
+            break;
+        step(1);
+        if (g == 0 && !finish())
+            break;
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitAll);  // no load into LDS outlives the workgroup
+}
+
 namespace {
+
+template <int kFormatA, bool kWide, int MT, int NT, int kAhead>
+zr_status split_run(const MatmulArgs &p, hipStream_t st)
+{
+    const int64_t tm = (p.m + 16 * MT - 1) / (16 * MT), tn = (p.n + 16 * NT - 1) / (16 * NT), tiles = tm * tn;
+    // enough waves for every SIMD twice, none without a group
+    int32_t split = kSplitWaves;
+    while (split > 1 && (tiles * split / 2 >= kCus * kSplitWaves || p.kb < split))
+        split /= 2;
+    const int64_t slots = kSplitWaves / split, rounds = (tiles + slots - 1) / slots;
+    return launch(matmul_split_kernel<kFormatA, kWide, MT, NT, kAhead>, grid_of(rounds), dim3(kSplitThreads), 0, st, p,
+                  split, tm, rounds);
+}
 
 template <int kFormatA, bool kWide>
 zr_status matmul_run(const MatmulArgs &p, hipStream_t st)
 {
-    if constexpr (!kWide) {
+    {
         const bool aligned = aligned_to(p.a, 16) && aligned_to(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0 &&
                              p.lda < (1 << 23) && p.ldb < (1 << 23) && p.m * p.kb < (1ll << 31) && p.n * p.kb < (1ll << 31);
-        if (aligned && p.kb > 1 && p.m > 256 && p.n >= 256) {
-            const int64_t bm = (p.m + kBig - 1) / kBig, bn = (p.n + kBig - 1) / kBig;
-            return launch(matmul_big_kernel<kFormatA>, grid_of(bm * bn < kCus ? bm * bn : kCus), dim3(kBlock), 0, st, p,
-                          (int32_t)bm, (int32_t)bn);
+        const int64_t bm = (p.m + kBig - 1) / kBig, bn = (p.n + kBig - 1) / kBig;
+        if constexpr (!kWide) {
+            if (aligned && p.kb > 1 && bm * bn >= kCus)
+                return launch(matmul_big_kernel<kFormatA>, grid_of(bm * bn < kCus ? bm * bn : kCus), dim3(kBlock), 0, st,
+                              p, (int32_t)bm, (int32_t)bn);
         }
+        const int64_t mm = (p.m + kMid - 1) / kMid, mn = (p.n + kMid - 1) / kMid;
+        if (aligned && p.kb > 0 && p.m > 64)
+            return launch(matmul_mid_kernel<kFormatA, kWide>, grid_of(mm * mn < kCus ? mm * mn : kCus), dim3(kBlock), 0,
+                          st, p, (int32_t)mm, (int32_t)mn);
     }
-    const int64_t tn = (p.n + kAnyTile - 1) / kAnyTile, tiles = tn * ((p.m + kAnyTile - 1) / kAnyTile);
-    return launch(matmul_any_kernel<kFormatA, kWide>, grid_of(tiles), dim3(kBlock), 0, st, p, tn, tiles);
+    if (p.m <= 16)
+        return split_run<kFormatA, kWide, 1, 1, 4>(p, st);
+    if (p.m <= 32)
+        return split_run<kFormatA, kWide, 2, 2, 2>(p, st);
+    return split_run<kFormatA, kWide, 4, 4, 1>(p, st);
 }
 
 }  // namespace
