@@ -382,13 +382,13 @@ constexpr int kScaleBlock = 4 * kBig * 4;     // LDS bytes of four groups' scale
 __device__ __forceinline__ int staged(int row, int piece) { return row * kGroup + ((piece ^ (row >> 1 & 7)) << 4); }
 
 // 16 (or 4) bytes of each lane from `rsrc` at byte `at` + `k` into LDS from byte `to`
-// on, lane after lane.  No register is written; the caller waits on vmcnt.  In
+// + `plus` (a constant) on, lane after lane.  No register is written; the caller waits on vmcnt.  In
 // assembly because the compiler would wait for every such load before any read of
 // the same LDS array, also of another stage.
-__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t at, int k, uint32_t to)
+__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t at, int k, uint32_t to, int plus)
 {
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 :: "v"(at), "s"(rsrc), "s"(k), "s"(to));
+    asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(at), "s"(rsrc), "s"(k), "s"(to), "i"(plus) : "scc");
 }
 
 __device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t at, uint32_t to)
@@ -491,8 +491,8 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
     };
     const auto load_piece = [&](uint32_t stage, int j) {  // j-th of 16 pieces of this wave
         const BigOperand &o = j & 1 ? oa : ob;
-        load16_to_lds(o.rsrc, o.at[j / 2], load_g * kGroup,
-                      lds0 + stage + (j & 1 ? 0 : kOperandStage) + j / 2 * 4096 + wave * 1024);
+        load16_to_lds(o.rsrc, o.at[j / 2], load_g * kGroup, lds0 + stage + wave * 1024,
+                      (j & 1 ? 0 : kOperandStage) + j / 2 * 4096);
     };
     const auto load_done = [&]() {
         if (load_g % 4 == 0) {
@@ -750,11 +750,12 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
     };
     const auto load_piece = [&](uint32_t stage, int j) {  // j-th of 8 pieces of this wave
         load16_to_lds(j & 1 ? ra : rb, j & 1 ? at_a[j / 2] : at_b[j / 2], load_g * kGroup,
-                      lds0 + stage + (j & 1 ? 0 : kMidOperand) + j / 2 * 4096 + wave * 1024);
+                      lds0 + stage + wave * 1024, (j & 1 ? 0 : kMidOperand) + j / 2 * 4096);
     };
     const auto load_done = [&]() {
         if (load_g % 8 == 0) {
-            load16_to_lds(wave < 2 ? rsa : rsb, (at_s + (uint32_t)load_g) & ~3u, 0, words0 + load_words + wave * 1024);
+            load16_to_lds(wave < 2 ? rsa : rsb, (at_s + (uint32_t)load_g) & ~3u, 0, words0 + load_words + wave * 1024,
+                          0);
             load_words = load_words == (kMidWordRing - 1) * kMidWords ? 0 : load_words + kMidWords;
         }
         if (++load_g == kb) {
@@ -798,8 +799,10 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
 #pragma unroll
         for (int y = 0; y < 4; ++y)
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
+            for (int z = 0; z < 4; ++z) {
                 acc[y][z] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                asm volatile("" : "+a"(acc[y][z]));  // in the registers that the products use
+            }
     };
 
     int32_t tile = blockIdx.x;
@@ -855,7 +858,7 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
                 acc[y][z] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                     operand(f[e].b[z][0], f[e].b[z][1]), operand(f[e].a[y][0], f[e].a[y][1]), acc[y][z], ZR_E4M3,
                     kFormatA, 0, (int)cb[e][z], 0, (int)ca[e][y]);
-                asm volatile("" : "+v"(acc[y][z]));
+                asm volatile("" : "+a"(acc[y][z]));
             } else {  // 8 codes of each lane, one row of tiles
                 const int q = i >> 2, y = i & 3, h = q / 2, c = q % 2 * 2;
                 if (y == 0)
@@ -866,14 +869,16 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                     acc[y][z] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[z], a, acc[y][z], 0, 0, 0);
-                    asm volatile("" : "+v"(acc[y][z]));
+                    asm volatile("" : "+a"(acc[y][z]));
                 }
             }
-            read_one(next, e ^ 1, i);
-            if (i & 1)
-                load_piece(stage, i / 2);
-            else
-                read_scale(e ^ 1, i / 2, gn);
+            if (i < 8) {
+                read_one(next, e ^ 1, 2 * i);
+                read_one(next, e ^ 1, 2 * i + 1);
+                read_scale(e ^ 1, i, gn);
+            } else {
+                load_piece(stage, i - 8);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
         load_done();
@@ -882,6 +887,9 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
         __builtin_amdgcn_s_waitcnt(kWaitRing);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
+#pragma unroll
+        for (int x = 0; x < 4; ++x)  // whole words from here on, not bytes to be widened at every use
+            asm volatile("" : "+v"(ca[e ^ 1][x]), "+v"(cb[e ^ 1][x]));
         if (tail && two + 1 == kb)
             clear_tail((stage + 2 * kMidStage) % (kRing * kMidStage));
         two = two + 1 == kb ? 0 : two + 1;
