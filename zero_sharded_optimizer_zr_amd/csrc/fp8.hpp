@@ -50,12 +50,13 @@ __device__ __forceinline__ uint16_t narrow(float x)
 }
 
 // Eight elements at p as four words; elements `n` and later are 0.  kAligned:
-// p is 16-byte aligned, so a whole vector is one load.
-template <bool kAligned>
+// p is 16-byte aligned, so a whole vector is one load.  kStream, here and below:
+// the access carries the non-temporal hint.
+template <bool kAligned, bool kStream = false>
 __device__ __forceinline__ u32x4 load8(const uint16_t *p, int64_t n)
 {
     if (kAligned && n >= kVec)
-        return *(global_ptr<const u32x4>)p;
+        return kStream ? load_stream(reinterpret_cast<const u32x4 *>(p)) : *(global_ptr<const u32x4>)p;
     u32x4 w = {0, 0, 0, 0};
 #pragma unroll
     for (int e = 0; e < kVec; ++e)
@@ -64,11 +65,14 @@ __device__ __forceinline__ u32x4 load8(const uint16_t *p, int64_t n)
     return w;
 }
 
-template <bool kAligned>
+template <bool kAligned, bool kStream = false>
 __device__ __forceinline__ void store8(uint16_t *p, u32x4 w, int64_t n)
 {
     if (kAligned && n >= kVec) {
-        *(global_ptr<u32x4>)p = w;
+        if (kStream)
+            store_stream(reinterpret_cast<u32x4 *>(p), w);
+        else
+            *(global_ptr<u32x4>)p = w;
         return;
     }
 #pragma unroll
@@ -78,11 +82,14 @@ __device__ __forceinline__ void store8(uint16_t *p, u32x4 w, int64_t n)
 }
 
 // Eight codes at p (8-byte aligned when kAligned), the first n of them.
-template <bool kAligned>
+template <bool kAligned, bool kStream = true>
 __device__ __forceinline__ void store_codes8(uint8_t *p, u32x2 w, int64_t n)
 {
     if (kAligned && n >= kVec) {
-        *(global_ptr<u32x2>)p = w;
+        if (kStream)
+            store_stream(reinterpret_cast<u32x2 *>(p), w);
+        else
+            *(global_ptr<u32x2>)p = w;
         return;
     }
 #pragma unroll

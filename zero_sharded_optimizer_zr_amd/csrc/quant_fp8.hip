@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(QuantArgs a, int6
 {
     const int lane = threadIdx.x & 63;
     const int64_t stride = (int64_t)gridDim.x * (kBlock / 16);
-    int64_t base = (int64_t)blockIdx.x * (kBlock / 16) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 4;
+    int64_t base = first_tile<64>() * (kBlock / 16) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 4;
     for (; base < groups; base += stride) {
         // row and group of the wave's first group, then of this lane's
         int64_t row = 0, g = base;
@@ -73,9 +73,9 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(QuantArgs a, int6
         const bool live = row < a.rows;
         const int64_t col = g * kGroup + (lane & 15) * kVec;
         const int64_t n = live ? a.cols - col : 0;
-        const u32x4 w = load8<kAligned>(a.src + row * a.ld + col, n);
+        const u32x4 w = load8<kAligned, true>(a.src + row * a.ld + col, n);
         const uint32_t s = scale_byte<kFormat>(wide_bits<T>(group_max(amax8(w))));
-        store_codes8<kAligned>(a.q + row * a.ldq + col, codes8<T, kFormat>(w, s), n);
+        store_codes8<kAligned, false>(a.q + row * a.ldq + col, codes8<T, kFormat>(w, s), n);
         if (live && (lane & 15) == 0)
             a.scales[row * a.gc + g] = (uint8_t)s;
     }
@@ -96,13 +96,13 @@ __global__ __launch_bounds__(kBlock) void quantize_tile_kernel(QuantArgs a, int6
     __shared__ u32x2 turn[kGroup * 16];
     __shared__ u32x4 colmax[4][16];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, tr = t >> 4, tc = t & 15;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    for (int64_t tile = first_tile<16>(); tile < tiles; tile += gridDim.x) {
         const int64_t gcol = tile / a.gr, grow = tile - gcol * a.gr;
         const int64_t r0 = grow * kGroup + tr * kVec, c0 = gcol * kGroup + tc * kVec;
         u32x4 w[kVec];
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            w[i] = load8<kAligned>(a.src + (r0 + i) * a.ld + c0, r0 + i < a.rows ? a.cols - c0 : 0);
+            w[i] = load8<kAligned, true>(a.src + (r0 + i) * a.ld + c0, r0 + i < a.rows ? a.cols - c0 : 0);
         // column maxima over this thread's rows, over the wave's, over the tile's
         u32x4 cm;
 #pragma unroll

@@ -69,7 +69,7 @@ __device__ __forceinline__ void norm_outputs(const NormArgs &a, int64_t row, int
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             o[i] = T::pack(y[2 * i], y[2 * i + 1]);
-        store8<kAligned>(a.y + row * a.ldy + c, o, n);
+        store8<kAligned, true>(a.y + row * a.ldy + c, o, n);
     }
     if (a.q) {
         uint32_t amax = 0;
@@ -123,8 +123,68 @@ __global__ __launch_bounds__(kBlock) void norm_wide_kernel(NormArgs a)
             if (r)
                 h = stream8<T>(h, load8<kAligned>(r + c, n));
             if (a.h)
-                store8<kAligned>(a.h + row * a.ldh + c, h, n);
+                store8<kAligned, true>(a.h + row * a.ldh + c, h, n);
             norm_outputs<T, kAligned>(a, row, c, n, h, load8<kAligned>(a.weight + c, n), rstd);
+        }
+    }
+}
+
+// Rows held in registers, read once: kWaves waves share a row, a lane holds NV vectors
+// of 8 columns, each wave-wide access covers 512 consecutive columns (four groups).
+template <typename T, int NV, int kWaves>
+__global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : kBlock) void norm_row_kernel(NormArgs a)
+{
+    constexpr int kThreads = kWaves > 4 ? 64 * kWaves : kBlock, kSlots = kThreads / (64 * kWaves);
+    __shared__ float part[2][kThreads / 64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int slot = wave / kWaves, w0 = wave % kWaves;
+    int flip = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * kSlots; row0 < a.rows; row0 += (int64_t)gridDim.x * kSlots, flip ^= 1) {
+        const int64_t row = row0 + slot;
+        const bool live = row < a.rows;
+        u32x4 h[NV], w[NV];
+        int32_t n[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int32_t c = ((v * kWaves + w0) * 64 + lane) * kVec;
+            n[v] = live ? (int32_t)a.cols - c : 0;
+            h[v] = load8<true>(a.x + row * a.ldx + c, n[v]);
+        }
+        if (a.residual) {
+            u32x4 r[NV];
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                r[v] = load8<true>(a.residual + row * a.ldr + ((v * kWaves + w0) * 64 + lane) * kVec, n[v]);
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                h[v] = stream8<T>(h[v], r[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            w[v] = load8<true>(a.weight + ((v * kWaves + w0) * 64 + lane) * kVec, n[v]);
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            sum = squares8<T>(h[v], sum);
+        sum = wave_sum(sum);
+        if constexpr (kWaves > 1) {
+            if (lane == 0)
+                part[flip][wave] = sum;
+            __syncthreads();
+            sum = part[flip][slot * kWaves];
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i)
+                sum += part[flip][slot * kWaves + i];
+        }
+        const float rstd = rstd_of(sum, a.cols, a.eps);
+        if (a.rstd && live && w0 == 0 && lane == 0)
+            a.rstd[row] = rstd;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int64_t c = ((v * kWaves + w0) * 64 + lane) * kVec;
+            if (a.h)
+                store8<true, true>(a.h + row * a.ldh + c, h[v], n[v]);
+            norm_outputs<T, true>(a, row, c, n[v], h[v], w[v], rstd);
         }
     }
 }
@@ -187,7 +247,7 @@ __global__ __launch_bounds__(kBlock) void norm_dx_wide_kernel(NormGradArgs a)
         for (int64_t c = threadIdx.x * kVec; c < a.cols; c += kBlock * kVec) {
             const int64_t n = a.cols - c;
             const u32x4 dh = a.dh ? load8<kAligned>(a.dh + row * a.lddh + c, n) : u32x4{0, 0, 0, 0};
-            store8<kAligned>(a.dx + row * a.lddx + c,
+            store8<kAligned, true>(a.dx + row * a.lddx + c,
                              dx8<T>(load8<kAligned>(dy + c, n), load8<kAligned>(a.weight + c, n),
                                     load8<kAligned>(h + c, n), dh, rstd, k), n);
         }
@@ -210,32 +270,205 @@ __global__ __launch_bounds__(kBlock) void norm_dweight_partial_kernel(NormGradAr
     }
 }
 
-// dweight from the partial sums.
-template <typename T>
-__global__ __launch_bounds__(kBlock) void norm_dweight_kernel(NormGradArgs a)
+// Rows held in registers, read once, for dx and the weight gradient together: kWaves
+// waves share a row, a workgroup takes kSlots rows at a time, every parts * kSlots'th,
+// and reads the next rows before it reduces the present ones.  A lane sums the weight
+// gradient of its columns over its rows; the slots meet in LDS, in slot order.
+constexpr int kGradThreads = 512;
+
+template <typename T, int NV, int kWaves>
+__global__ __launch_bounds__(kGradThreads) void norm_grad_row_kernel(NormGradArgs a)
 {
-    for (int64_t c = global_tid(); c < a.cols; c += grid_stride()) {
+    constexpr int kSlots = kGradThreads / (64 * kWaves), kCols = NV * kWaves * 64 * kVec;
+    constexpr bool kEarly = NV <= 2;  // two rows of 4 vectors to a lane are more than the registers hold
+    __shared__ float part[2][kGradThreads / 64];
+    __shared__ f32x4 sums[kSlots > 1 ? (kSlots - 1) * kCols / 4 : 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int slot = wave / kWaves, w0 = wave % kWaves;
+    int32_t c[NV], n[NV];
+    u32x4 w[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        c[v] = ((v * kWaves + w0) * 64 + lane) * kVec;
+        n[v] = (int32_t)a.cols - c[v];
+        w[v] = load8<true>(a.weight + c[v], n[v]);
+    }
+    const int64_t stride = a.parts * kSlots;
+    for (int64_t p = blockIdx.x; p < a.parts; p += gridDim.x) {
+        f32x4 dw[NV][2];
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            dw[v][0] = dw[v][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        u32x4 dy[NV], h[NV], dh[NV];
+        float rstd = 0.0f;
+        const auto load = [&](int64_t row) {
+            const bool live = row < a.rows;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                dy[v] = load8<true>(a.dy + row * a.lddy + c[v], live ? n[v] : 0);
+                h[v] = load8<true>(a.h + row * a.ldh + c[v], live ? n[v] : 0);
+                dh[v] = a.dh ? load8<true>(a.dh + row * a.lddh + c[v], live ? n[v] : 0) : u32x4{0, 0, 0, 0};
+            }
+            rstd = live ? a.rstd[row] : 0.0f;
+        };
+        int flip = 0;
+        // the same number of rounds in every slot
+        load(p * kSlots + slot);
+        for (int64_t row0 = p * kSlots; row0 < a.rows; row0 += stride, flip ^= 1) {
+            const int64_t row = row0 + slot;
+            float sum = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                sum = dots8<T>(dy[v], w[v], h[v], sum);
+            u32x4 o_dy[NV], o_h[NV], o_dh[NV];
+            const float r = rstd;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                o_dy[v] = dy[v];
+                o_h[v] = h[v];
+                o_dh[v] = dh[v];
+            }
+            if constexpr (kEarly)
+                load(row + stride);
+            sum = wave_sum(sum);
+            if constexpr (kWaves > 1) {
+                if (lane == 0)
+                    part[flip][wave] = sum;
+                __syncthreads();
+                sum = part[flip][slot * kWaves];
+#pragma unroll
+                for (int i = 1; i < kWaves; ++i)
+                    sum += part[flip][slot * kWaves + i];
+            }
+            const float k = dx_factor(sum, r, a.cols);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float *d = reinterpret_cast<float *>(&dw[v][i / 2]) + i % 2 * 2;
+                    d[0] = __builtin_fmaf(T::lo(o_dy[v][i]), T::lo(o_h[v][i]) * r, d[0]);
+                    d[1] = __builtin_fmaf(T::hi(o_dy[v][i]), T::hi(o_h[v][i]) * r, d[1]);
+                }
+                if (row < a.rows)
+                    store8<true, true>(a.dx + row * a.lddx + c[v], dx8<T>(o_dy[v], w[v], o_h[v], o_dh[v], r, k), n[v]);
+            }
+            if constexpr (!kEarly)
+                load(row + stride);
+        }
+        if constexpr (kSlots > 1) {
+            __syncthreads();
+            if (slot > 0) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    sums[(slot - 1) * (kCols / 4) + c[v] / 4] = dw[v][0];
+                    sums[(slot - 1) * (kCols / 4) + c[v] / 4 + 1] = dw[v][1];
+                }
+            }
+            __syncthreads();
+        }
+        if (slot == 0) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+#pragma unroll
+                for (int s = 1; s < kSlots; ++s) {
+                    dw[v][0] += sums[(s - 1) * (kCols / 4) + c[v] / 4];
+                    dw[v][1] += sums[(s - 1) * (kCols / 4) + c[v] / 4 + 1];
+                }
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (e < n[v])
+                        a.partial[p * a.cols + c[v] + e] = dw[v][e / 4][e % 4];
+            }
+        }
+    }
+}
+
+// dweight from the partial sums: 32 columns (a line) to a workgroup, 16 threads to a
+// column, each over every 16th partial sum; they meet in LDS in that order.
+template <typename T>
+__global__ __launch_bounds__(kGradThreads) void norm_dweight_kernel(NormGradArgs a)
+{
+    __shared__ float part[16][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < a.cols; c0 += (int64_t)gridDim.x * 32) {
+        const int64_t c = c0 + x;
         float sum = 0.0f;
-        for (int64_t p = 0; p < a.parts; ++p)
-            sum += a.partial[p * a.cols + c];
-        a.dweight[c] = narrow<T>(sum);
+        if (c < a.cols)
+#pragma unroll 8
+            for (int64_t p = y; p < a.parts; p += 16)
+                sum += a.partial[p * a.cols + c];
+        part[y][x] = sum;
+        __syncthreads();
+        if (y == 0 && c < a.cols) {
+#pragma unroll
+            for (int i = 1; i < 16; ++i)
+                sum += part[i][x];
+            a.dweight[c] = narrow<T>(sum);
+        }
+        __syncthreads();
     }
 }
 
 namespace {
 
+template <typename T, int NV, int kWaves>
+zr_status norm_rows(const NormArgs &a, hipStream_t st)
+{
+    constexpr int threads = kWaves > 4 ? 64 * kWaves : kBlock, slots = threads / (64 * kWaves);
+    return launch(norm_row_kernel<T, NV, kWaves>, grid_of((a.rows + slots - 1) / slots), dim3(threads), 0, st, a);
+}
+
+// Two vectors to a lane as long as that takes at most 8 waves, then more: enough
+// loads in flight, and a row of up to 16384 columns fits the registers.
 template <typename T>
 zr_status norm_run(const NormArgs &a, bool aligned, hipStream_t st)
 {
     const dim3 grid = grid_of(a.rows);
-    return aligned ? launch(norm_wide_kernel<T, true>, grid, dim3(kBlock), 0, st, a)
-                   : launch(norm_wide_kernel<T, false>, grid, dim3(kBlock), 0, st, a);
+    if (!aligned)
+        return launch(norm_wide_kernel<T, false>, grid, dim3(kBlock), 0, st, a);
+    if (a.cols <= 512)
+        return norm_rows<T, 1, 1>(a, st);
+    if (a.cols <= 1024)
+        return norm_rows<T, 1, 2>(a, st);
+    if (a.cols <= 2048)
+        return norm_rows<T, 1, 4>(a, st);
+    if (a.cols <= 4096)
+        return norm_rows<T, 2, 4>(a, st);
+    if (a.cols <= 8192)
+        return norm_rows<T, 2, 8>(a, st);
+    if (a.cols <= 16384)
+        return norm_rows<T, 4, 8>(a, st);
+    return launch(norm_wide_kernel<T, true>, grid, dim3(kBlock), 0, st, a);
+}
+
+template <typename T, int NV, int kWaves>
+zr_status norm_grad_rows(NormGradArgs a, hipStream_t st)
+{
+    constexpr int slots = kGradThreads / (64 * kWaves);
+    const int64_t rounds = (a.rows + slots - 1) / slots;
+    a.parts = rounds < ZR_RMSNORM_PARTIALS ? rounds : ZR_RMSNORM_PARTIALS;
+    const zr_status s = launch(norm_grad_row_kernel<T, NV, kWaves>, grid_of(a.parts), dim3(kGradThreads), 0, st, a);
+    return s != ZR_OK ? s : launch(norm_dweight_kernel<T>, grid_of((a.cols + 31) / 32), dim3(kGradThreads), 0, st, a);
 }
 
 template <typename T>
-zr_status norm_backward_run(const NormGradArgs &a, bool aligned, hipStream_t st)
+zr_status norm_backward_run(NormGradArgs a, bool aligned, hipStream_t st)
 {
+    if (a.rows > 0 && aligned && a.cols <= 16384) {
+        if (a.cols <= 512)
+            return norm_grad_rows<T, 1, 1>(a, st);
+        if (a.cols <= 1024)
+            return norm_grad_rows<T, 2, 1>(a, st);
+        if (a.cols <= 2048)
+            return norm_grad_rows<T, 2, 2>(a, st);
+        if (a.cols <= 4096)
+            return norm_grad_rows<T, 2, 4>(a, st);
+        if (a.cols <= 8192)
+            return norm_grad_rows<T, 2, 8>(a, st);
+        return norm_grad_rows<T, 4, 8>(a, st);
+    }
     zr_status s = ZR_OK;
+    a.parts = a.rows < ZR_RMSNORM_PARTIALS ? a.rows : ZR_RMSNORM_PARTIALS;
     if (a.rows > 0) {
         // dweight's partial sums first: dx may replace dy
         const int64_t blocks = (a.cols + kBlock - 1) / kBlock * a.parts;
@@ -244,9 +477,7 @@ zr_status norm_backward_run(const NormGradArgs &a, bool aligned, hipStream_t st)
             s = aligned ? launch(norm_dx_wide_kernel<T, true>, grid_of(a.rows), dim3(kBlock), 0, st, a)
                         : launch(norm_dx_wide_kernel<T, false>, grid_of(a.rows), dim3(kBlock), 0, st, a);
     }
-    if (s == ZR_OK)
-        s = launch(norm_dweight_kernel<T>, grid_of((a.cols + kBlock - 1) / kBlock), dim3(kBlock), 0, st, a);
-    return s;
+    return s != ZR_OK ? s : launch(norm_dweight_kernel<T>, grid_of((a.cols + 31) / 32), dim3(kGradThreads), 0, st, a);
 }
 
 // A matrix of 16-bit elements on 16-byte boundaries in every row.
@@ -346,7 +577,7 @@ extern "C" zr_status zr_rmsnorm_backward(const void *dy, int64_t lddy, const voi
     const NormGradArgs a{static_cast<const uint16_t *>(dy), static_cast<const uint16_t *>(h),
                          static_cast<const uint16_t *>(weight), static_cast<const uint16_t *>(dh), rstd, lddy, ldh,
                          lddh, rows, cols, static_cast<uint16_t *>(dx), static_cast<uint16_t *>(dweight), lddx,
-                         workspace, rows < ZR_RMSNORM_PARTIALS ? rows : ZR_RMSNORM_PARTIALS};
+                         workspace, 0};
     const bool aligned = rows_aligned(dy, lddy, rows) && rows_aligned(h, ldh, rows) && aligned_to(weight, 16) &&
                          rows_aligned(dh, lddh, rows) && rows_aligned(dx, lddx, rows);
     hipStream_t st = static_cast<hipStream_t>(stream);
