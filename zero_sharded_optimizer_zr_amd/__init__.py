@@ -636,9 +636,17 @@ _SCALES = (torch.float8_e8m0fnu, torch.uint8)
 def _shape(t: torch.Tensor, name: str) -> Tuple[int, int]:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() not in (1, 2):
+    shape = t.shape
+    if len(shape) == 2:
+        return tuple(shape)
+    if len(shape) != 1:
         raise ValueError(f"{name} must have one or two dimensions")
-    return (1, t.shape[0]) if t.dim() == 1 else tuple(t.shape)
+    return 1, shape[0]
+
+
+def _typed(t: torch.Tensor, dtypes, name: str) -> None:
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
 
 
 def _matrix(t: Optional[torch.Tensor], dtypes, name: str, shape: Optional[Tuple[int, int]] = None):
@@ -646,18 +654,18 @@ def _matrix(t: Optional[torch.Tensor], dtypes, name: str, shape: Optional[Tuple[
     a 1-D tensor as one row.  (None, 0) for None."""
     if t is None:
         return None, 0
-    rows, cols = _shape(t, name)
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if shape is not None and (rows, cols) != shape:
+    rows, cols = own = _shape(t, name)
+    _typed(t, dtypes, name)
+    if shape is not None and own != shape:
         raise ValueError(f"{name} is {rows} x {cols}, {shape[0]} x {shape[1]} needed")
-    if cols > 1 and t.stride(-1) != 1:
+    strides = t.stride()
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have contiguous rows")
     if rows <= 1:
         return t.data_ptr() or None, cols
-    if t.stride(0) < cols:
+    if strides[0] < cols:
         raise ValueError(f"{name} must not have overlapping rows")
-    return t.data_ptr() or None, t.stride(0)
+    return t.data_ptr() or None, strides[0]
 
 
 def _vector(t: Optional[torch.Tensor], dtypes, n: int, name: str) -> Optional[int]:
@@ -666,13 +674,26 @@ def _vector(t: Optional[torch.Tensor], dtypes, n: int, name: str) -> Optional[in
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    _typed(t, dtypes, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if t.numel() < n:
         raise ValueError(f"{name} holds {t.numel()} elements, {n} needed")
     return t.data_ptr() or None
+
+
+def _gpu_call_flat(fn, stream, tensors, *args) -> None:
+    """_gpu_call for a flat tuple of tensors (or None), at less cost per call: these
+    operators also run on single rows, where the call is longer than the kernel."""
+    devices = {t.get_device() for t in tensors if t is not None}
+    if stream is None and len(devices) == 1 and torch.cuda.is_initialized():
+        device = devices.pop()
+        if device == torch._C._cuda_getDevice():
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+            if status != ZR_OK:
+                raise ZRError(status, zr_last_error())
+            return
+    _gpu_call(fn, stream, tensors, *args)
 
 
 def _groups(n: int) -> int:
@@ -713,7 +734,7 @@ def zr_quantize_fp8(src: torch.Tensor, q: Optional[torch.Tensor] = None, scales:
     down, across = (rows, cols) if block_rows == 1 else (_groups(rows), _groups(cols))
     p_s = _vector(scales, _SCALES, down * _groups(cols), "scales")
     p_st = _vector(scales_t, _SCALES, across * _groups(rows), "scales_t")
-    _gpu_call(_lib.zr_quantize_fp8, stream, (src, q, scales, qt, scales_t), p_src, _DTYPES[src.dtype], rows, cols, ld,
+    _gpu_call_flat(_lib.zr_quantize_fp8, stream, (src, q, scales, qt, scales_t), p_src, _DTYPES[src.dtype], rows, cols, ld,
               int(block_rows), _FORMATS[one.dtype], p_q, ldq, p_s, p_qt, ldqt, p_st)
 
 
@@ -730,7 +751,7 @@ def zr_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sc
     p_out, ldo = _matrix(out, _DTYPES, "out", (m, n))
     p_sa = _vector(a_scales, _SCALES, m * _groups(k), "a_scales")
     p_sb = _vector(b_scales, _SCALES, (n if b_block_rows == 1 else _groups(n)) * _groups(k), "b_scales")
-    _gpu_call(_lib.zr_matmul_fp8, stream, (a, a_scales, b, b_scales, out), p_a, lda, p_sa, _FORMATS[a.dtype], p_b, ldb,
+    _gpu_call_flat(_lib.zr_matmul_fp8, stream, (a, a_scales, b, b_scales, out), p_a, lda, p_sa, _FORMATS[a.dtype], p_b, ldb,
               p_sb, int(b_block_rows), m, n, k, p_out, _DTYPES[out.dtype], ldo, int(bool(accumulate)))
 
 
@@ -753,7 +774,7 @@ def zr_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, y: Optional[torch.Tens
     p_w = _vector(weight, same, cols, "weight")
     p_s = _vector(scales, _SCALES, rows * _groups(cols), "scales")
     p_rstd = _vector(rstd, (torch.float32,), rows, "rstd")
-    _gpu_call(_lib.zr_rmsnorm_fp8, stream, (x, residual, weight, h, y, q, scales, rstd), p_x, ldx, p_r, ldr, p_w,
+    _gpu_call_flat(_lib.zr_rmsnorm_fp8, stream, (x, residual, weight, h, y, q, scales, rstd), p_x, ldx, p_r, ldr, p_w,
               _DTYPES[x.dtype], rows, cols, float(eps), p_h, ldh, p_y, ldy, p_q, ldq, p_s, p_rstd)
 
 
@@ -772,5 +793,5 @@ def zr_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     p_w, p_dw = _vector(weight, same, cols, "weight"), _vector(dweight, same, cols, "dweight")
     p_rstd = _vector(rstd, (torch.float32,), rows, "rstd")
     p_ws = _vector(workspace, (torch.float32,), ZR_RMSNORM_PARTIALS * cols, "workspace")
-    _gpu_call(_lib.zr_rmsnorm_backward, stream, (dy, h, weight, rstd, dx, dweight, workspace, dh), p_dy, lddy, p_h, ldh,
+    _gpu_call_flat(_lib.zr_rmsnorm_backward, stream, (dy, h, weight, rstd, dx, dweight, workspace, dh), p_dy, lddy, p_h, ldh,
               p_w, p_rstd, p_dh, lddh, _DTYPES[h.dtype], rows, cols, p_dx, lddx, p_dw, p_ws)

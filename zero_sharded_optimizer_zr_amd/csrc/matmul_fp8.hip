@@ -942,28 +942,49 @@ zr_status split_run(const MatmulArgs &p, hipStream_t st)
                   split, tm, rounds);
 }
 
+// Which kernel.  Times in us on MI355X, operands rotated through more than the caches:
+//  - A split wave's tile is the smallest that leaves at most one workgroup to a compute
+//    unit.  1 x 4096 x 4096: 16 x 16 outputs 6.8, 16 x 32 8.4, 32 x 32 9.3; 1 x 11008 x 4096
+//    (m x n x k): 14.5, 14.3 and, with 16 x 64, 13.6; 32 x 11008 x 4096: 32 x 32 22, 32 x 64
+//    17.5; 64 x 4096 x 4096: 32 x 32 12.2, 64 x 64 20.6.
+//  - More tiles than that go to the LDS kernels (333 x 4096 x 4096: 64 x 64 39, 128 x 128 22),
+//    up to 16 rows excepted, which are bound by B's bytes either way (1 x 32000 x 4096:
+//    16 x 32 25.5, 5.1 TB/s).
+//  - A round of 256 x 256 tiles costs 9/4 rounds of 128 x 128 (one round each, k = 4096: 50
+//    and 22; 2048 x 4096 x 4096: 54 against 48 for two; 4096 x 4096 x 4096: 64 against 98 for four).
+// The LDS kernels load 16 bytes at a time and index a tile's rows in 32 bits; what does
+// not meet that stays with the split waves.
 template <int kFormatA, bool kWide>
 zr_status matmul_run(const MatmulArgs &p, hipStream_t st)
 {
-    {
-        const bool aligned = aligned_to(p.a, 16) && aligned_to(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0 &&
-                             p.lda < (1 << 23) && p.ldb < (1 << 23) && p.m * p.kb < (1ll << 31) && p.n * p.kb < (1ll << 31);
-        const int64_t bm = (p.m + kBig - 1) / kBig, bn = (p.n + kBig - 1) / kBig;
-        if constexpr (!kWide) {
-            if (aligned && p.kb > 1 && bm * bn >= kCus)
-                return launch(matmul_big_kernel<kFormatA>, grid_of(bm * bn < kCus ? bm * bn : kCus), dim3(kBlock), 0, st,
-                              p, (int32_t)bm, (int32_t)bn);
-        }
-        const int64_t mm = (p.m + kMid - 1) / kMid, mn = (p.n + kMid - 1) / kMid;
-        if (aligned && p.kb > 0 && p.m > 64)
-            return launch(matmul_mid_kernel<kFormatA, kWide>, grid_of(mm * mn < kCus ? mm * mn : kCus), dim3(kBlock), 0,
-                          st, p, (int32_t)mm, (int32_t)mn);
-    }
+    const auto tiles = [&](int64_t rows, int64_t cols) {
+        return ((p.m + rows - 1) / rows) * ((p.n + cols - 1) / cols);
+    };
+    const auto rounds = [](int64_t n) { return (n + kCus - 1) / kCus; };
+    const bool aligned = aligned_to(p.a, 16) && aligned_to(p.b, 16) && (p.lda % 16 == 0 || p.m == 1) &&
+                         (p.ldb % 16 == 0 || p.n == 1) && p.lda < (1 << 23) && p.ldb < (1 << 23) &&
+                         p.m * p.kb < (1ll << 31) && p.n * p.kb < (1ll << 31) && p.kb > 0;
+    if (tiles(16, 16) <= kCus)
+        return split_run<kFormatA, kWide, 1, 1, 2>(p, st);
+    if (tiles(16, 32) <= kCus)
+        return split_run<kFormatA, kWide, 1, 2, 2>(p, st);
     if (p.m <= 16)
-        return split_run<kFormatA, kWide, 1, 1, 4>(p, st);
-    if (p.m <= 32)
+        return tiles(16, 64) <= kCus ? split_run<kFormatA, kWide, 1, 4, 2>(p, st)
+                                     : split_run<kFormatA, kWide, 1, 2, 2>(p, st);
+    if (tiles(32, 32) <= kCus)
         return split_run<kFormatA, kWide, 2, 2, 2>(p, st);
-    return split_run<kFormatA, kWide, 4, 4, 1>(p, st);
+    if (tiles(32, 64) <= kCus)
+        return split_run<kFormatA, kWide, 2, 4, 2>(p, st);
+    if (!aligned || tiles(64, 64) <= kCus)
+        return split_run<kFormatA, kWide, 4, 4, 1>(p, st);
+    const int64_t big = tiles(kBig, kBig), mid = tiles(kMid, kMid);
+    if constexpr (!kWide) {
+        if (p.kb > 1 && 9 * rounds(big) <= 4 * rounds(mid))
+            return launch(matmul_big_kernel<kFormatA>, grid_of(big < kCus ? big : kCus), dim3(kBlock), 0, st, p,
+                          (int32_t)((p.m + kBig - 1) / kBig), (int32_t)((p.n + kBig - 1) / kBig));
+    }
+    return launch(matmul_mid_kernel<kFormatA, kWide>, grid_of(mid < kCus ? mid : kCus), dim3(kBlock), 0, st, p,
+                  (int32_t)((p.m + kMid - 1) / kMid), (int32_t)((p.n + kMid - 1) / kMid));
 }
 
 }  // namespace
