@@ -60,7 +60,11 @@ def check(got, a, sa, b, sb, block_rows, start=None):
 SIZES = [(1, 1, 1), (1, 16, 128), (1, 128, 4096), (3, 100, 1000), (7, 4096, 512), (8, 2048, 2048), (16, 300, 640),
          (17, 257, 4096), (33, 511, 1040), (64, 64, 8192), (65, 640, 2000), (100, 1000, 272), (128, 128, 128), (129, 384, 1920),
          (250, 300, 5008), (256, 256, 4096), (257, 513, 1152), (300, 2048, 96), (512, 768, 2304), (1000, 520, 1008),
-         (777, 1500, 400), (1024, 2048, 512), (2048, 1280, 1040), (1024, 4096, 144), (640, 33, 1024)]
+         (777, 1500, 400), (1024, 2048, 512), (2048, 1280, 1040), (1024, 4096, 144), (640, 33, 1024),
+         # every shape of a split wave's tile
+         (24, 4096, 384), (16, 11008, 256), (9, 32000, 300), (60, 3900, 400), (32, 11008, 256), (100, 4096, 384), (250, 4000, 640),
+         # the 128 x 128 ring and the 256 x 256 tiles: edges, one to several tiles a workgroup
+         (1100, 1030, 100), (1100, 1030, 2176), (2300, 2000, 656), (2900, 2950, 400), (2817, 2945, 1040), (4100, 2100, 272), (5000, 5300, 200)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
@@ -75,7 +79,8 @@ def test_sizes(m, n, k):
         check(run(a, sa, b, sb, block_rows, dtype), a, sa, b, sb, block_rows)
 
 
-@pytest.mark.parametrize("m,n,k", [(5, 200, 700), (70, 300, 700), (300, 400, 1000), (300, 400, 3), (1100, 1030, 1100)])
+@pytest.mark.parametrize("m,n,k", [(5, 200, 700), (70, 300, 700), (300, 400, 1000), (300, 400, 3), (1100, 1030, 1100),
+                                   (2900, 2950, 300)])
 @pytest.mark.parametrize("lda,ldb,ldo,offset", [(0, 0, 0, 0), (16, 32, 8, 0), (5, 0, 3, 0), (0, 9, 0, 0), (0, 0, 0, 1), (16, 16, 4, 16)])
 def test_strides_and_alignment(m, n, k, lda, ldb, ldo, offset):
     """Row distances of k or n plus the given pads (the third shape's rows as odd as k),
@@ -88,7 +93,8 @@ def test_strides_and_alignment(m, n, k, lda, ldb, ldo, offset):
         check(run(a, sa, b, sb, 128, dtype, n + ldo, offset), a, sa, b, sb, 128)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 300, 512), (20, 300, 512), (200, 300, 512), (1100, 1030, 512), (1100, 1030, 0), (4, 30, 0)])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 512), (20, 300, 512), (200, 300, 512), (1100, 1030, 512), (1100, 1030, 0), (4, 30, 0),
+                                   (2900, 2950, 272)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 def test_accumulate(m, n, k, dtype):
     device()
@@ -99,7 +105,7 @@ def test_accumulate(m, n, k, dtype):
     check(run(a, sa, b, sb, 1, dtype), a, sa, b, sb, 1)
 
 
-@pytest.mark.parametrize("m,n,k", [(2, 200, 300), (90, 200, 300), (300, 400, 300), (1100, 1030, 304)])
+@pytest.mark.parametrize("m,n,k", [(2, 200, 300), (90, 200, 300), (300, 400, 300), (1100, 1030, 304), (2900, 2950, 304)])
 def test_every_code_and_scale(m, n, k):
     """Random bytes as codes (no NaN) and scales over a wide range, zeros among the codes."""
     device()
@@ -114,54 +120,59 @@ def test_every_code_and_scale(m, n, k):
         check(run(a, sa, b, sb, 128, torch.float32), a, sa, b, sb, 128)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 1, 200), (2, 200, 200), (90, 200, 200), (300, 400, 200), (1100, 1030, 208)])
+@pytest.mark.parametrize("m,n,k", [(1, 1, 200), (2, 200, 200), (90, 200, 200), (300, 400, 200), (1100, 1030, 208),
+                                   (1100, 1030, 100), (1100, 1030, 391), (2900, 2950, 200), (2900, 2950, 391)])
 def test_what_lies_behind_a_row_is_not_read_into_it(m, n, k):
     """NaN codes behind every row's end, in the pad and behind the matrix, change nothing."""
     device()
-    ld = 256
+    ld = max(256, groups(k) * 128)
     a, sa = operand(m, k, E4M3, 1, 7, ld)
     b, sb = operand(n, k, E4M3, 1, 8, ld)
-    want = run(a, sa, b, sb, 1, torch.float32).clone()
+    want = [run(a, sa, b, sb, 1, t).clone() for t in (torch.float32, torch.bfloat16)]
     for g in (a, b):
         keep = g.view.view(torch.uint8).clone()
         g.raw.fill_(0x7f)
         g.view.view(torch.uint8).copy_(keep)
-    out = torch.empty(m, n, device="cuda")
-    zr.zr_matmul_fp8(a.view, sa, b.view, sb, out, b_block_rows=1)
-    assert torch.equal(out, want)
+    for w in want:
+        out = torch.empty_like(w)
+        zr.zr_matmul_fp8(a.view, sa, b.view, sb, out, b_block_rows=1)
+        assert torch.equal(out, w)
 
 
-@pytest.mark.parametrize("m,n,k", [(3, 300, 1000), (70, 300, 1000), (300, 400, 1000), (1100, 1030, 1008)])
+@pytest.mark.parametrize("m,n,k", [(3, 300, 1000), (70, 300, 1000), (300, 400, 1000), (1100, 1030, 1008), (2900, 2950, 400)])
 def test_nan_scales_and_codes_stay_in_their_rows(m, n, k):
     device()
     a, sa = operand(m, k, E4M3, 1, 9, groups(k) * 128)
     b, sb = operand(n, k, E4M3, 1, 10, groups(k) * 128)
-    want = run(a, sa, b, sb, 1, torch.float32).clone()
+    want = [run(a, sa, b, sb, 1, t).clone() for t in (torch.float32, torch.bfloat16)]
     sa[1, groups(k) - 1] = 255
     sb[n - 2, 0] = 255
     b.view.view(torch.uint8)[5, 130] = 0x7f
-    got = run(a, sa, b, sb, 1, torch.float32)
     nan = torch.zeros(m, n, dtype=torch.bool, device="cuda")
     nan[1], nan[:, n - 2], nan[:, 5] = True, True, True
-    assert torch.equal(got.isnan(), nan)
-    assert torch.equal(got[~nan], want[~nan])
+    for w in want:
+        got = run(a, sa, b, sb, 1, w.dtype)
+        assert torch.equal(got.isnan(), nan)
+        assert torch.equal(got[~nan], w[~nan])
 
 
-@pytest.mark.parametrize("m,n,k", [(2, 300, 512), (90, 300, 512), (300, 400, 512), (1100, 1030, 512)])
+@pytest.mark.parametrize("m,n,k", [(2, 300, 512), (90, 300, 512), (300, 400, 512), (1100, 1030, 512), (2900, 2950, 512)])
 def test_results_do_not_depend_on_the_other_rows(m, n, k):
     """A row's product is the same bits wherever its operands lie and on every call."""
     device()
     a, sa = operand(m, k, E4M3, 1, 11)
     b, sb = operand(n, k, E4M3, 1, 12)
-    first = run(a, sa, b, sb, 1, torch.float32).clone()
-    assert torch.equal(run(a, sa, b, sb, 1, torch.float32), first)
     perm = torch.randperm(m, generator=torch.Generator().manual_seed(1)).cuda()
-    moved, _ = Guarded(m, k, E4M3, None, 0, a.view.view(torch.uint8)[perm]), None
-    assert torch.equal(run(moved, sa.cuda()[perm].contiguous(), b, sb, 1, torch.float32), first[perm])
+    moved = Guarded(m, k, E4M3, None, 0, a.view.view(torch.uint8)[perm])
+    for dtype in (torch.float32, torch.bfloat16):
+        first = run(a, sa, b, sb, 1, dtype).clone()
+        assert torch.equal(run(a, sa, b, sb, 1, dtype), first)
+        assert torch.equal(run(moved, sa.cuda()[perm].contiguous(), b, sb, 1, dtype), first[perm])
 
 
 @pytest.mark.parametrize("cap", ["8", "24"])
-@pytest.mark.parametrize("m,n,k", [(2, 1000, 1100), (90, 1000, 1104), (700, 1000, 1104), (1100, 2060, 1104), (700, 1000, 1101)])
+@pytest.mark.parametrize("m,n,k", [(2, 1000, 1100), (90, 1000, 1104), (700, 1000, 1104), (1100, 2060, 1104), (700, 1000, 1101),
+                                   (2900, 2950, 400)])
 def test_capped_grid(monkeypatch, m, n, k, cap):
     device()
     a, sa = operand(m, k, E4M3, 1, 13)
