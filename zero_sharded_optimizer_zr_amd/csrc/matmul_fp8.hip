@@ -834,6 +834,7 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         read_scale(0, i, 0);
+    __syncthreads();  // every wave has read the first group before another is loaded into its place
     uint32_t stage = 0;
     int32_t g = 0, two = 2 % kb;  // the group that is multiplied, and the one two stages on
 
