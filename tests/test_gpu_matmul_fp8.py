@@ -64,7 +64,11 @@ SIZES = [(1, 1, 1), (1, 16, 128), (1, 128, 4096), (3, 100, 1000), (7, 4096, 512)
          # every shape of a split wave's tile
          (24, 4096, 384), (16, 11008, 256), (9, 32000, 300), (60, 3900, 400), (32, 11008, 256), (100, 4096, 384), (250, 4000, 640),
          # the 128 x 128 ring and the 256 x 256 tiles: edges, one to several tiles a workgroup
-         (1100, 1030, 100), (1100, 1030, 2176), (2300, 2000, 656), (2900, 2950, 400), (2817, 2945, 1040), (4100, 2100, 272), (5000, 5300, 200)]
+         (1100, 1030, 100), (1100, 1030, 2176), (2300, 2000, 656), (1500, 2050, 400), (2900, 2950, 400),
+         (2817, 2945, 1040), (4100, 2100, 272), (5000, 5300, 200),
+         # 128 x 64 by two teams: one group, odd numbers of groups, short last groups
+         (300, 4100, 128), (200, 5000, 100), (390, 4100, 300), (250, 4100, 1040), (129, 4500, 2100), (250, 4100, 4000),
+         (1500, 2050, 100), (1500, 2050, 1300)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
@@ -80,7 +84,7 @@ def test_sizes(m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(5, 200, 700), (70, 300, 700), (300, 400, 1000), (300, 400, 3), (1100, 1030, 1100),
-                                   (2900, 2950, 300)])
+                                   (1500, 2050, 300), (2900, 2950, 300)])
 @pytest.mark.parametrize("lda,ldb,ldo,offset", [(0, 0, 0, 0), (16, 32, 8, 0), (5, 0, 3, 0), (0, 9, 0, 0), (0, 0, 0, 1), (16, 16, 4, 16)])
 def test_strides_and_alignment(m, n, k, lda, ldb, ldo, offset):
     """Row distances of k or n plus the given pads (the third shape's rows as odd as k),
@@ -93,8 +97,9 @@ def test_strides_and_alignment(m, n, k, lda, ldb, ldo, offset):
         check(run(a, sa, b, sb, 128, dtype, n + ldo, offset), a, sa, b, sb, 128)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 300, 512), (20, 300, 512), (200, 300, 512), (1100, 1030, 512), (1100, 1030, 0), (4, 30, 0),
-                                   (2900, 2950, 272)])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 512), (20, 300, 512), (200, 300, 512), (1100, 1030, 512),
+                                   (1100, 1030, 0), (4, 30, 0),
+                                   (1500, 2050, 272), (2900, 2950, 272)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 def test_accumulate(m, n, k, dtype):
     device()
@@ -105,7 +110,8 @@ def test_accumulate(m, n, k, dtype):
     check(run(a, sa, b, sb, 1, dtype), a, sa, b, sb, 1)
 
 
-@pytest.mark.parametrize("m,n,k", [(2, 200, 300), (90, 200, 300), (300, 400, 300), (1100, 1030, 304), (2900, 2950, 304)])
+@pytest.mark.parametrize("m,n,k", [(2, 200, 300), (90, 200, 300), (300, 400, 300), (1100, 1030, 304),
+                                   (1500, 2050, 304), (2900, 2950, 304)])
 def test_every_code_and_scale(m, n, k):
     """Random bytes as codes (no NaN) and scales over a wide range, zeros among the codes."""
     device()
@@ -121,7 +127,7 @@ def test_every_code_and_scale(m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 1, 200), (2, 200, 200), (90, 200, 200), (300, 400, 200), (1100, 1030, 208),
-                                   (1100, 1030, 100), (1100, 1030, 391), (2900, 2950, 200), (2900, 2950, 391)])
+                                   (1100, 1030, 100), (1100, 1030, 391), (1500, 2050, 200), (2900, 2950, 200), (1500, 2050, 391), (2900, 2950, 391)])
 def test_what_lies_behind_a_row_is_not_read_into_it(m, n, k):
     """NaN codes behind every row's end, in the pad and behind the matrix, change nothing."""
     device()
@@ -139,7 +145,8 @@ def test_what_lies_behind_a_row_is_not_read_into_it(m, n, k):
         assert torch.equal(out, w)
 
 
-@pytest.mark.parametrize("m,n,k", [(3, 300, 1000), (70, 300, 1000), (300, 400, 1000), (1100, 1030, 1008), (2900, 2950, 400)])
+@pytest.mark.parametrize("m,n,k", [(3, 300, 1000), (70, 300, 1000), (300, 400, 1000), (1100, 1030, 1008),
+                                   (1500, 2050, 400), (2900, 2950, 400)])
 def test_nan_scales_and_codes_stay_in_their_rows(m, n, k):
     device()
     a, sa = operand(m, k, E4M3, 1, 9, groups(k) * 128)
@@ -156,7 +163,8 @@ def test_nan_scales_and_codes_stay_in_their_rows(m, n, k):
         assert torch.equal(got[~nan], w[~nan])
 
 
-@pytest.mark.parametrize("m,n,k", [(2, 300, 512), (90, 300, 512), (300, 400, 512), (1100, 1030, 512), (2900, 2950, 512)])
+@pytest.mark.parametrize("m,n,k", [(2, 300, 512), (90, 300, 512), (300, 400, 512), (1100, 1030, 512),
+                                   (1500, 2050, 512), (2900, 2950, 512)])
 def test_results_do_not_depend_on_the_other_rows(m, n, k):
     """A row's product is the same bits wherever its operands lie and on every call."""
     device()
@@ -171,8 +179,9 @@ def test_results_do_not_depend_on_the_other_rows(m, n, k):
 
 
 @pytest.mark.parametrize("cap", ["8", "24"])
-@pytest.mark.parametrize("m,n,k", [(2, 1000, 1100), (90, 1000, 1104), (700, 1000, 1104), (1100, 2060, 1104), (700, 1000, 1101),
-                                   (2900, 2950, 400)])
+@pytest.mark.parametrize("m,n,k", [(2, 1000, 1100), (90, 1000, 1104), (700, 1000, 1104), (1100, 2060, 1104),
+                                   (700, 1000, 1101),
+                                   (1500, 2050, 400), (2900, 2950, 400)])
 def test_capped_grid(monkeypatch, m, n, k, cap):
     device()
     a, sa = operand(m, k, E4M3, 1, 13)

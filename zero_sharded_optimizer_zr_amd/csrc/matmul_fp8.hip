@@ -928,6 +928,237 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
     __builtin_amdgcn_s_waitcnt(kWaitAll);  // no load into LDS outlives the workgroup
 }
 
+// ------------------------------------------------ few tiles, a long summed axis --
+
+// A workgroup computes 128 x 64 outputs with two teams of four waves, one for each half
+// of the groups: a wave of a team computes 64 x 32, two waves to a SIMD, so that one
+// multiplies while the other issues its loads.  Each team has a ring of three groups of
+// both operands in LDS; at the end the teams' sums meet there, each team stores half.
+// Against four waves alone: a single wave to a SIMD issues its ~110 instructions of a
+// group one after another, 0.41 us for 0.11 us of products (333 x 4096 x 11008: 41.6 us,
+// 128 x 128 outputs 52); the teams take 38 us, now bound by the loads (24 us with the same
+// loop that loads nothing; 32 us with operands in the last-level cache).  Bringing lines
+// into the L2 ahead of the loads, shared out or not, made it slower (43, 52 us).
+constexpr int kPairRows = 128, kPairCols = 64;
+constexpr int kPairThreads = 512;
+constexpr int kPairRing = 3;
+constexpr int kPairOperand = kPairRows * kGroup;                  // LDS bytes of a group of A
+constexpr int kPairStage = (kPairRows + kPairCols) * kGroup;      // of both operands
+constexpr int kPairWords = 256 * 16;                              // of eight groups' scales
+constexpr int kPairWait = 0x0076;  // s_waitcnt vmcnt(6) lgkmcnt(0): all but the last stage
+
+template <int kFormatA, bool kWide>
+__global__ __launch_bounds__(kPairThreads, 2) void matmul_pair_kernel(MatmulArgs p, int32_t tiles_m, int32_t tiles_n)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kPairRing * kPairStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t words[2 * 2 * kPairWords];
+    const int t = threadIdx.x & 255, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int team = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 32, row = lane & 15, quad = lane >> 4;
+    const int32_t tiles = tiles_m * tiles_n, kb = (int32_t)p.kb, half = (kb + 1) / 2;
+    const int32_t first = team * half, count = team ? kb - half : half;
+    const int tail = (int)(p.k % kGroup), tail_team = kb > 1, tail_at = kb > 1 ? kb - half - 1 : 0;
+    typedef __attribute__((address_space(3))) uint8_t *lds_address;
+    const uint32_t base = (uint32_t)team * (kPairRing * kPairStage), word_base = (uint32_t)team * (2 * kPairWords);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_address)lds + base + (uint32_t)wave * 1024;
+    const uint32_t words0 = (uint32_t)(uintptr_t)(lds_address)words + word_base;
+
+    // Scales: the 16 bytes from the word on that holds a row's first byte of eight
+    // groups; words behind the array's last one read as zeros.
+    const uint32_t low_a = (uint32_t)(uintptr_t)p.sa & 3, low_b = (uint32_t)(uintptr_t)p.sb & 3;
+    const auto rsa = buffer(p.sa - low_a, (p.m * kb + low_a + 3) & ~3ll);
+    const auto rsb = buffer(p.sb - low_b, ((((p.n - 1) >> p.b_shift) + 1) * kb + low_b + 3) & ~3ll);
+
+    for (int32_t v = blockIdx.x; v < tiles; v += gridDim.x) {
+        // one run of tiles per XCD, down the columns of tiles: they share their rows of B
+        const int32_t x = v % kXcds, each = tiles / kXcds, more = tiles % kXcds;
+        const int32_t tile = x * each + (x < more ? x : more) + v / kXcds;
+        const int64_t i0 = (int64_t)(tile % tiles_m) * kPairRows, j0 = (int64_t)(tile / tiles_m) * kPairCols;
+
+        // The loader.  Rows that do not exist are replaced by the last one, and so are
+        // groups behind the team's last one, which nothing uses.
+        const int here_a = (int)(p.m - i0 < kPairRows ? p.m - i0 : kPairRows);
+        const int here_b = (int)(p.n - j0 < kPairCols ? p.n - j0 : kPairCols);
+        const auto ra = buffer(p.a + i0 * p.lda, ((here_a - 1) * p.lda + p.k + 15) & ~15ll);
+        const auto rb = buffer(p.b + j0 * p.ldb, ((here_b - 1) * p.ldb + p.k + 15) & ~15ll);
+        uint32_t at[6];
+#pragma unroll
+        for (int j = 0; j < 6; ++j) {
+            const int r = (j < 4 ? j : j - 4) * 32 + (t >> 3);
+            at[j] = (j < 4 ? row_at(r, here_a, p.lda) : row_at(r, here_b, p.ldb)) + ((uint32_t)((t & 7) ^ (r >> 1 & 7)) << 4);
+        }
+        // waves 0 and 1 bring A's scales, wave 2 B's
+        const uint32_t scale_row = wave < 2 ? (uint32_t)i0 + (uint32_t)(t < here_a ? t : here_a - 1)
+                                            : (uint32_t)(j0 + (lane < here_b ? lane : here_b - 1)) >> p.b_shift;
+        const uint32_t at_s = scale_row * (uint32_t)kb + (wave < 2 ? low_a : low_b) + (uint32_t)first;
+        const auto group_at = [&](int32_t g) { return (first + (g < count ? g : count - 1)) * kGroup; };
+        const auto load_piece = [&](uint32_t stage, int32_t g, int j) {
+            load16_to_lds(j < 4 ? ra : rb, at[j], group_at(g), lds0 + stage, j * 4096);
+        };
+        const auto load_scales = [&](int32_t g) {  // of the eight groups from g on
+            if (wave < 3)
+                load16_to_lds(wave < 2 ? rsa : rsb, (at_s + (uint32_t)g) & ~3u, 0,
+                              words0 + (uint32_t)(g & 8) * (kPairWords / 8) + (uint32_t)wave * 1024, 0);
+        };
+        // Zeros in place of what lies behind the rows' ends in the last group.
+        const auto clear_tail = [&](uint32_t stage) {
+            for (int q = t < kPairRows + kPairCols ? tail / 4 : kGroup / 4; q < kGroup / 4; ++q) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(lds + base + stage + staged(t, q / 4) + q % 4 * 4);
+                *w = q == tail / 4 ? *w & ((1u << (8 * (tail % 4))) - 1u) : 0u;
+            }
+        };
+
+        SplitGroup<4, 2> f[2];
+        uint32_t ca[2][4], cb[2][2];
+        f32x4 acc[4][2];
+        // i-th of 12 reads of the operands of the group at `stage`
+        const auto read_one = [&](uint32_t stage, int e, int i) {
+            const bool b = i < 8 && i % 2 == 0;
+            const int j = i < 8 ? i / 2 : i - 4, x = j / 2, piece = quad + j % 2 * 4;
+            (b ? f[e].b[x] : f[e].a[x])[j % 2] = *reinterpret_cast<const u32x4 *>(
+                lds + base + stage + staged((b ? kPairRows + wn : wm) + x * 16 + row, piece));
+        };
+        // this lane's bytes in eight groups' scales; rows 16 apart start at the same byte of a word
+        const uint32_t ia = (uint32_t)i0 + wm + row, jb = (uint32_t)(j0 + wn + row) >> p.b_shift;
+        const uint32_t first_a = word_base + (uint32_t)(wm + row) * 16 + ((ia * (uint32_t)kb + low_a + first) & 3);
+        const uint32_t first_b = word_base + (uint32_t)(kPairRows + wn + row) * 16 + ((jb * (uint32_t)kb + low_b + first) & 3);
+        const auto read_scale = [&](int e, int i, int32_t g) {  // i-th of 6
+            const uint8_t *w = words + (uint32_t)(g & 8) * (kPairWords / 8) + (g & 7);
+            if (i < 2)
+                cb[e][i] = w[first_b + i * 256];
+            else
+                ca[e][i - 2] = w[first_a + (i - 2) * 256];
+        };
+
+#pragma unroll
+        for (int s = 0; s < kPairRing; ++s) {
+#pragma unroll
+            for (int j = 0; j < 6; ++j)
+                load_piece(s * kPairStage, s, j);
+            if (s == 0)
+                load_scales(0);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                acc[y][z] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                asm volatile("" : "+a"(acc[y][z]));  // in the registers that the products use
+            }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(kWaitAll);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (tail && tail_at <= 1) {
+            if (team == tail_team)
+                clear_tail(tail_at * kPairStage);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < 12; ++i)
+            read_one(0, 0, i);
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            read_scale(0, i, 0);
+        __syncthreads();  // every wave has read the first group before another is loaded into its place
+        uint32_t stage = 0;
+        int32_t g = 0;
+
+        // Group g is multiplied from registers e while the next group's operands are read
+        // into the other ones and the group kPairRing on is loaded into g's place.
+        const auto step = [&](int e) {
+            const uint32_t next = stage == (kPairRing - 1) * kPairStage ? 0 : stage + kPairStage;
+            constexpr int kParts = kWide ? 16 : 8, kHalf = kParts / 2;
+            bf16x8 b[2], a;
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                if constexpr (!kWide) {
+                    const int y = i / 2, z = i % 2;
+                    acc[y][z] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        operand(f[e].b[z][0], f[e].b[z][1]), operand(f[e].a[y][0], f[e].a[y][1]), acc[y][z], ZR_E4M3,
+                        kFormatA, 0, (int)cb[e][z], 0, (int)ca[e][y]);
+                    asm volatile("" : "+a"(acc[y][z]));
+                } else {  // 8 codes of each lane, one row of tiles
+                    const int q = i >> 2, y = i & 3, h = q / 2, c = q % 2 * 2;
+                    if (y == 0)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z)
+                            b[z] = widen8<ZR_E4M3>(f[e].b[z][h][c], f[e].b[z][h][c + 1], __uint_as_float(cb[e][z] << 23));
+                    a = widen8<kFormatA>(f[e].a[y][h][c], f[e].a[y][h][c + 1], __uint_as_float(ca[e][y] << 23));
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        acc[y][z] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[z], a, acc[y][z], 0, 0, 0);
+                        asm volatile("" : "+a"(acc[y][z]));
+                    }
+                }
+                if (i < kHalf) {
+#pragma unroll
+                    for (int x = i * 6 / kHalf; x < (i + 1) * 6 / kHalf; ++x)
+                        load_piece(stage, g + kPairRing, x);
+                }
+                if (i == kHalf && (g + kPairRing) % 8 == 0)
+                    load_scales(g + kPairRing);
+#pragma unroll
+                for (int x = i * 12 / kParts; x < (i + 1) * 12 / kParts; ++x)
+                    read_one(next, e ^ 1, x);
+#pragma unroll
+                for (int x = i * 6 / kParts; x < (i + 1) * 6 / kParts; ++x)
+                    read_scale(e ^ 1, x, g + 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // two stages on has landed, in every wave, and the next one has been read by all
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(kPairWait);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {  // whole words from here on, not bytes to be widened at every use
+                asm volatile("" : "+v"(ca[e ^ 1][x]));
+                if (x < 2)
+                    asm volatile("" : "+v"(cb[e ^ 1][x]));
+            }
+            if (tail && tail_at == g + 2) {
+                if (team == tail_team)
+                    clear_tail(next == (kPairRing - 1) * kPairStage ? 0 : next + kPairStage);
+                __syncthreads();
+            }
+            stage = next;
+            ++g;
+        };
+        for (;;) {
+            if (g >= count)
+                break;
+            step(0);
+            if (g >= count)
+                break;
+            step(1);
+        }
+        if (count < half)  // the other team's last step
+            __builtin_amdgcn_s_barrier();
+
+        // The teams' sums: each hands half of its rows to the other.
+        __builtin_amdgcn_s_waitcnt(kWaitAll);  // no load into LDS is under way
+        __syncthreads();
+        f32x4 *const swap = reinterpret_cast<f32x4 *>(lds) + wave * 64 + lane;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+                swap[(team * 4 + y * 2 + z) * 256] = team ? acc[y][z] : acc[y + 2][z];
+        __syncthreads();
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const f32x4 v4 = (team ? acc[y + 2][z] : acc[y][z]) + swap[((team ^ 1) * 4 + y * 2 + z) * 256];
+                const int64_t i = i0 + wm + (y + team * 2) * 16 + row, j = j0 + wn + z * 16 + quad * 4;
+                if (i < p.m)
+                    store_out(p, i, j, v4, p.n - j);
+            }
+        __syncthreads();  // before the next tile's loads
+    }
+}
+
 namespace {
 
 template <int kFormatA, bool kWide, int MT, int NT, int kAhead>
@@ -947,10 +1178,13 @@ zr_status split_run(const MatmulArgs &p, hipStream_t st)
 //  - A split wave's tile is the smallest that leaves at most one workgroup to a compute
 //    unit.  1 x 4096 x 4096: 16 x 16 outputs 6.8, 16 x 32 8.4, 32 x 32 9.3; 1 x 11008 x 4096
 //    (m x n x k): 14.5, 14.3 and, with 16 x 64, 13.6; 32 x 11008 x 4096: 32 x 32 22, 32 x 64
-//    17.5; 64 x 4096 x 4096: 32 x 32 12.2, 64 x 64 20.6.
-//  - More tiles than that go to the LDS kernels (333 x 4096 x 4096: 64 x 64 39, 128 x 128 22),
-//    up to 16 rows excepted, which are bound by B's bytes either way (1 x 32000 x 4096:
-//    16 x 32 25.5, 5.1 TB/s).
+//    17.5; 64 x 4096 x 4096: 32 x 32 12.2, 64 x 64 20.6; 128 x 4096 x 4096: 32 x 64 16.8, two teams 18.2.
+//  - More tiles than that go to the LDS kernels (250 x 4096 x 11008: 64 x 64 a wave 45, 128 x 64
+//    and two teams 39), up to 16 rows excepted, which are bound by B's bytes either way
+//    (1 x 32000 x 4096: 16 x 32 25.5, 5.1 TB/s).
+//  - One round of 128 x 64 tiles goes to the two teams: 333 x 4096 x 4096 18.5 (128 x 128 by four
+//    waves 24.5), with fp32 outputs 23 (39); 1000 x 1000 x 4000 15.3 (64 x 64 a wave 21.3).  Two
+//    rounds of them lose to one of 128 x 128: 1000 x 4096 x 4096 37.5 and 29 (fp32 53 and 47).
 //  - A round of 256 x 256 tiles costs 9/4 rounds of 128 x 128 (one round each, k = 4096: 50
 //    and 22; 2048 x 4096 x 4096: 54 against 48 for two; 4096 x 4096 x 4096: 64 against 98 for four).
 // The LDS kernels load 16 bytes at a time and index a tile's rows in 32 bits; what does
@@ -976,8 +1210,12 @@ zr_status matmul_run(const MatmulArgs &p, hipStream_t st)
         return split_run<kFormatA, kWide, 2, 2, 2>(p, st);
     if (tiles(32, 64) <= kCus)
         return split_run<kFormatA, kWide, 2, 4, 2>(p, st);
-    if (!aligned || tiles(64, 64) <= kCus)
+    if (!aligned)
         return split_run<kFormatA, kWide, 4, 4, 1>(p, st);
+    const int64_t pair = tiles(kPairRows, kPairCols);
+    if (pair <= kCus)
+        return launch(matmul_pair_kernel<kFormatA, kWide>, grid_of(pair), dim3(kPairThreads), 0, st, p,
+                      (int32_t)((p.m + kPairRows - 1) / kPairRows), (int32_t)((p.n + kPairCols - 1) / kPairCols));
     const int64_t big = tiles(kBig, kBig), mid = tiles(kMid, kMid);
     if constexpr (!kWide) {
         if (p.kb > 1 && 9 * rounds(big) <= 4 * rounds(mid))
