@@ -32,7 +32,9 @@
  * allocation, capturable into a zr_graph.  Matrices are row-major; `ld` arguments
  * are the distance between rows in elements (>= the row length).  Buffers need
  * their element's natural alignment only; matrices whose base and row distance
- * are multiples of 16 bytes take the vector paths, with the same results.
+ * are multiples of 16 bytes take the vector paths.  The same call gives the same
+ * bits every time; the order of fp32 sums, and with it their last bit, goes by
+ * the call's sizes and by that alignment, never by the machine's state.
  * Buffers that a call writes must not overlap any other of its buffers (as
  * address ranges from the first to the last element) except where stated.
  * Calls with disjoint outputs may run at once on different streams.
@@ -139,10 +141,10 @@ ZR_API zr_status zr_rmsnorm_fp8(const void *x, int64_t ldx, const void *residual
  *   dweight[j] = sum over rows of dy * xh
  * dh (NULL for none) is the gradient that reaches the stream h from the layers
  * above; dx is the gradient of x and of residual alike.  dx may be exactly dy or
- * dh with the same row distance.  Sums are fp32 in an order fixed by rows and
- * cols; each output is rounded once.  workspace: fp32 [ZR_RMSNORM_PARTIALS * cols], contents undefined
- * before and after; two calls that may run at once need workspaces of their
- * own.  rows == 0 writes dweight = 0 and nothing else.  cols >= 1.
+ * dh with the same row distance.  Sums are fp32; each output is rounded once.
+ * workspace: fp32 [ZR_RMSNORM_PARTIALS * cols], contents undefined before and
+ * after; two calls that may run at once need workspaces of their own, and so do
+ * two graphs whose replays may.  rows == 0 writes dweight = 0 and nothing else.  cols >= 1.
  * Errors: ZR_EINVAL, ZR_EALIGN, ZR_EHIP.
  */
 ZR_API zr_status zr_rmsnorm_backward(const void *dy, int64_t lddy, const void *h, int64_t ldh, const void *weight,

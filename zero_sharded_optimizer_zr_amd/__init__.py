@@ -734,8 +734,8 @@ def zr_quantize_fp8(src: torch.Tensor, q: Optional[torch.Tensor] = None, scales:
     down, across = (rows, cols) if block_rows == 1 else (_groups(rows), _groups(cols))
     p_s = _vector(scales, _SCALES, down * _groups(cols), "scales")
     p_st = _vector(scales_t, _SCALES, across * _groups(rows), "scales_t")
-    _gpu_call_flat(_lib.zr_quantize_fp8, stream, (src, q, scales, qt, scales_t), p_src, _DTYPES[src.dtype], rows, cols, ld,
-              int(block_rows), _FORMATS[one.dtype], p_q, ldq, p_s, p_qt, ldqt, p_st)
+    _gpu_call_flat(_lib.zr_quantize_fp8, stream, (src, q, scales, qt, scales_t), p_src, _DTYPES[src.dtype], rows,
+                   cols, ld, int(block_rows), _FORMATS[one.dtype], p_q, ldq, p_s, p_qt, ldqt, p_st)
 
 
 def zr_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
@@ -751,8 +751,9 @@ def zr_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sc
     p_out, ldo = _matrix(out, _DTYPES, "out", (m, n))
     p_sa = _vector(a_scales, _SCALES, m * _groups(k), "a_scales")
     p_sb = _vector(b_scales, _SCALES, (n if b_block_rows == 1 else _groups(n)) * _groups(k), "b_scales")
-    _gpu_call_flat(_lib.zr_matmul_fp8, stream, (a, a_scales, b, b_scales, out), p_a, lda, p_sa, _FORMATS[a.dtype], p_b, ldb,
-              p_sb, int(b_block_rows), m, n, k, p_out, _DTYPES[out.dtype], ldo, int(bool(accumulate)))
+    _gpu_call_flat(_lib.zr_matmul_fp8, stream, (a, a_scales, b, b_scales, out), p_a, lda, p_sa, _FORMATS[a.dtype],
+                   p_b, ldb, p_sb, int(b_block_rows), m, n, k, p_out, _DTYPES[out.dtype], ldo,
+                   int(bool(accumulate)))
 
 
 def zr_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, y: Optional[torch.Tensor] = None,
@@ -774,8 +775,8 @@ def zr_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, y: Optional[torch.Tens
     p_w = _vector(weight, same, cols, "weight")
     p_s = _vector(scales, _SCALES, rows * _groups(cols), "scales")
     p_rstd = _vector(rstd, (torch.float32,), rows, "rstd")
-    _gpu_call_flat(_lib.zr_rmsnorm_fp8, stream, (x, residual, weight, h, y, q, scales, rstd), p_x, ldx, p_r, ldr, p_w,
-              _DTYPES[x.dtype], rows, cols, float(eps), p_h, ldh, p_y, ldy, p_q, ldq, p_s, p_rstd)
+    _gpu_call_flat(_lib.zr_rmsnorm_fp8, stream, (x, residual, weight, h, y, q, scales, rstd), p_x, ldx, p_r, ldr,
+                   p_w, _DTYPES[x.dtype], rows, cols, float(eps), p_h, ldh, p_y, ldy, p_q, ldq, p_s, p_rstd)
 
 
 def zr_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -793,5 +794,5 @@ def zr_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     p_w, p_dw = _vector(weight, same, cols, "weight"), _vector(dweight, same, cols, "dweight")
     p_rstd = _vector(rstd, (torch.float32,), rows, "rstd")
     p_ws = _vector(workspace, (torch.float32,), ZR_RMSNORM_PARTIALS * cols, "workspace")
-    _gpu_call_flat(_lib.zr_rmsnorm_backward, stream, (dy, h, weight, rstd, dx, dweight, workspace, dh), p_dy, lddy, p_h, ldh,
-              p_w, p_rstd, p_dh, lddh, _DTYPES[h.dtype], rows, cols, p_dx, lddx, p_dw, p_ws)
+    _gpu_call_flat(_lib.zr_rmsnorm_backward, stream, (dy, h, weight, rstd, dx, dweight, workspace, dh), p_dy, lddy,
+                   p_h, ldh, p_w, p_rstd, p_dh, lddh, _DTYPES[h.dtype], rows, cols, p_dx, lddx, p_dw, p_ws)

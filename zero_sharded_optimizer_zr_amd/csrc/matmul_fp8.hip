@@ -18,6 +18,10 @@
 // output would keep that error, so its codes are widened to bf16 (exact: at most 3
 // mantissa bits; the scale is applied by the conversion), whose products the matrix
 // unit adds in fp32 (7e-8 off), at half the rate.
+//
+// Four kernels: waves that split the summed axis (few rows, any alignment), 128 x 64
+// outputs by two teams, 128 x 128 through a ring in LDS, and 256 x 256 for the large
+// products; matmul_run says which is taken when.
 #include "fp8.hpp"
 
 namespace zr {
@@ -161,14 +165,17 @@ __device__ __forceinline__ i32x8 operand(u32x4 lo, u32x4 hi)
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-// ------------------------------------------ few rows, fp32 outputs, any alignment --
+// ------------------------------------------------------- few rows, any alignment --
 
 // A wave computes 16 MT x 16 NT outputs over a range of groups, its operands loaded
 // straight into registers (a lane's 32 codes of a group are pieces `quad` and `quad`
 // + 4 of its row: 16 rows x 64 bytes an instruction), `kAhead` groups ahead of their
-// use.  kSplit waves of a workgroup share a tile and a kSplit-th of the groups each;
+// use.  `split` waves of a workgroup share a tile and take a part of the groups each;
 // their sums meet in LDS and are added in wave order.  So a product with few
-// tiles still occupies the chip, without a workspace.
+// tiles still occupies the chip, without a workspace.  Bound by the bytes of B and by
+// the latency of the few loads a wave makes: 1 x 11008 x 4096 (m x n x k) 13.6 us, 3.3
+// TB/s; 1 x 32000 x 4096 25.5 us, 5.1 TB/s; 64 x 11008 x 4096 22 us; 1 x 512 x 512 3.5 us,
+// a launch.
 constexpr int kSplitThreads = 512;
 constexpr int kSplitWaves = kSplitThreads / 64;
 
@@ -372,6 +379,18 @@ __global__ __launch_bounds__(kSplitThreads, 2) void matmul_split_kernel(MatmulAr
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+// A workgroup of four waves computes 256 x 256 outputs, a wave 128 x 128 (the accumulators
+// take half of a SIMD's registers; fewer outputs to a wave would read LDS more often than
+// it can answer).  A group of both operands is 64 KB of LDS; one is multiplied while the
+// next is loaded, and workgroups stay for several tiles, so that a tile's first loads fall
+// under the last products of the one before.
+//
+// Bound by power: with random codes the matrix unit alone, fed from registers, reaches 4.0
+// PFLOP/s of the 4.95 that it reaches with zeros, and with the loads beside it the clock
+// falls further, to 1.7 to 2.0 GHz.  16384 x 11008 x 4096: 632 us, 2.34 PFLOP/s; 16384 cubed
+// 2.6 PFLOP/s; 11008 x 4096 x 8111 (e5m2) 320 us.  Measured and not kept: 16 x 16 x 128
+// instructions (682 us at a state of 655), scales read as bytes so that nothing waits at mid-group (1.5 to
+// 3 % slower), results packed before they are turned (spills).
 constexpr int kBig = 256;                    // output rows and columns of a workgroup
 constexpr int kOperandStage = kBig * kGroup;  // LDS bytes of one group of one operand
 constexpr int kStage = 2 * kOperandStage;
@@ -454,7 +473,7 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
     const uint32_t words0 = (uint32_t)(uintptr_t)(lds_address)reinterpret_cast<uint8_t *>(words);
 
     const auto tile_at = [&](int32_t v, int64_t *i0, int64_t *j0) {
-        // one run of tiles per XCD; within it, strips of kStrip tile rows
+        // one run of tiles per XCD; within it, strips of kStrip tile rows (8 and 16: slower)
         constexpr int32_t kStrip = 4;
         const int32_t x = v % kXcds, each = tiles / kXcds, more = tiles % kXcds;
         const int32_t i = x * each + (x < more ? x : more) + v / kXcds;
@@ -517,7 +536,8 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
         }
     };
     // Brings the lines of the group kAhead further on into the L2, where the loads of
-    // the XCD's workgroups, which run side by side, would all wait for them.
+    // the XCD's workgroups, which run side by side, would all wait for them (12 % of the
+    // time).
     const auto prefetch = [&]() {
         constexpr int32_t kAhead = 1;
         const int32_t g = load_g + kAhead;
@@ -688,7 +708,11 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
 // A workgroup computes 128 x 128 outputs, a wave 64 x 64, through a ring of kRing
 // groups of both operands in LDS, with the operands of the next group read into
 // registers while one is multiplied.  For products with too few 256 x 256 tiles to
-// occupy the chip, and for fp32 outputs.
+// occupy the chip, and for fp32 outputs.  A group takes 0.5 us for 0.21 us of products:
+// the one wave of a SIMD issues reads, loads and control one after another (the order in
+// which they are spread between the products makes no difference).
+// 1000 x 4096 x 4096 27 us; fp32 outputs, bound by the matrix unit's bf16 rate and by the
+// widening: 11008 x 4096 x 8192 715 us, 1.03 PFLOP/s.
 constexpr int kMid = 128;
 constexpr int kRing = 4;
 constexpr int kMidOperand = kMid * kGroup;

