@@ -31,10 +31,11 @@
  * launched and nothing written on an error, asynchronous on `stream`, no device
  * allocation, capturable into a zr_graph.  Matrices are row-major; `ld` arguments
  * are the distance between rows in elements (>= the row length).  Buffers need
- * their element's natural alignment only; matrices whose base and row distance
- * are multiples of 16 bytes take the vector paths.  The same call gives the same
- * bits every time; the order of fp32 sums, and with it their last bit, goes by
- * the call's sizes and by that alignment, never by the machine's state.
+ * their element's natural alignment only; products of matrices of codes whose base
+ * and row distance are multiples of 16 bytes are the fast ones.  The same call gives
+ * the same bits every time; the order of a product's fp32 sums, and with it their
+ * last bit, goes by the call's sizes and by that alignment, never by the machine's
+ * state.
  * Buffers that a call writes must not overlap any other of its buffers (as
  * address ranges from the first to the last element) except where stated.
  * Calls with disjoint outputs may run at once on different streams.

@@ -703,7 +703,7 @@ def _groups(n: int) -> int:
 def fp8_matrix(rows: int, cols: int, dtype=torch.float8_e4m3fn, block_rows: int = 1,
                device=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(codes [rows, cols], scales) for the 8-bit operators, uninitialised; the
-    rows of codes start on 128-byte lines, so that every kernel takes its vector path."""
+    rows of codes start on 128-byte lines, as the fast products want them."""
     device = device if device is not None else "cuda"
     codes = torch.empty(rows, _groups(cols) * ZR_FP8_GROUP, dtype=dtype, device=device)[:, :cols]
     tall = rows if block_rows == 1 else _groups(rows)

@@ -966,9 +966,8 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
 constexpr int kPairRows = 128, kPairCols = 64;
 constexpr int kPairThreads = 512;
 constexpr int kPairRing = 3;
-constexpr int kPairOperand = kPairRows * kGroup;                  // LDS bytes of a group of A
-constexpr int kPairStage = (kPairRows + kPairCols) * kGroup;      // of both operands
-constexpr int kPairWords = 256 * 16;                              // of eight groups' scales
+constexpr int kPairStage = (kPairRows + kPairCols) * kGroup;  // LDS bytes of a group of both operands, A first
+constexpr int kPairWords = 256 * 16;                          // of eight groups' scales
 constexpr int kPairWait = 0x0076;  // s_waitcnt vmcnt(6) lgkmcnt(0): all but the last stage
 
 template <int kFormatA, bool kWide>

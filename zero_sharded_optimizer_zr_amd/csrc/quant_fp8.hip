@@ -53,7 +53,7 @@ __device__ __forceinline__ u32x2 codes8(u32x4 w, uint32_t s)
 // whole lines; the maximum is four DPP steps.  Each XCD takes 64 consecutive tiles of
 // 16 groups at a time: 8192 x 11008 bf16 in 50 us, 5.4 TB/s (in launch order 56 us).
 // 1 x 4096 takes 2 us, a launch.
-template <typename T, int kFormat, bool kAligned>
+template <typename T, int kFormat>
 __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(QuantArgs a, int64_t groups)
 {
     const int lane = threadIdx.x & 63;
@@ -76,9 +76,9 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(QuantArgs a, int6
         const bool live = row < a.rows;
         const int64_t col = g * kGroup + (lane & 15) * kVec;
         const int64_t n = live ? a.cols - col : 0;
-        const u32x4 w = load8<kAligned, true>(a.src + row * a.ld + col, n);
+        const u32x4 w = load8<true>(a.src + row * a.ld + col, n);
         const uint32_t s = scale_byte<kFormat>(wide_bits<T>(group_max(amax8(w))));
-        store_codes8<kAligned, false>(a.q + row * a.ldq + col, codes8<T, kFormat>(w, s), n);
+        store_codes8<false>(a.q + row * a.ldq + col, codes8<T, kFormat>(w, s), n);
         if (live && (lane & 15) == 0)
             a.scales[row * a.gc + g] = (uint8_t)s;
     }
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(QuantArgs a, int6
 // columns: 60 us, 4.1 TB/s: a row of a tile is 256 bytes of a source row and 128 of a
 // copy's, shorter runs than a copy's.  The 8 x 8 elements of a thread need the registers
 // of two workgroups to a compute unit: bounded to 4 or 5 they spill (92 and 120 us).
-template <typename T, int kFormat, bool kBlocks, bool kAligned>
+template <typename T, int kFormat, bool kBlocks>
 __global__ __launch_bounds__(kBlock) void quantize_tile_kernel(QuantArgs a, int64_t tiles)
 {
     __shared__ u32x2 turn[kGroup * 16];
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kBlock) void quantize_tile_kernel(QuantArgs a, int6
         u32x4 w[kVec];
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            w[i] = load8<kAligned, true>(a.src + (r0 + i) * a.ld + c0, r0 + i < a.rows ? a.cols - c0 : 0);
+            w[i] = load8<true>(a.src + (r0 + i) * a.ld + c0, r0 + i < a.rows ? a.cols - c0 : 0);
         // column maxima over this thread's rows, over the wave's, over the tile's
         u32x4 cm;
 #pragma unroll
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(kBlock) void quantize_tile_kernel(QuantArgs a, int6
             for (int i = 0; i < kVec; ++i) {
                 const uint32_t s = kBlocks ? block : scale_byte<kFormat>(wide_bits<T>(group_max(amax8(w[i]))));
                 if (r0 + i < a.rows) {
-                    store_codes8<kAligned>(a.q + (r0 + i) * a.ldq + c0, codes8<T, kFormat>(w[i], s), a.cols - c0);
+                    store_codes8(a.q + (r0 + i) * a.ldq + c0, codes8<T, kFormat>(w[i], s), a.cols - c0);
                     if (!kBlocks && tc == 0)
                         a.scales[(r0 + i) * a.gc + gcol] = (uint8_t)s;
                 }
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kBlock) void quantize_tile_kernel(QuantArgs a, int6
             const int col = tr + 16 * p;
             const int64_t c = gcol * kGroup + col, r = grow * kGroup + tc * kVec;
             if (c < a.cols)
-                store_codes8<kAligned>(a.qt + c * a.ldqt + r, turn[col * 16 + (tc ^ (col >> 3))], a.rows - r);
+                store_codes8(a.qt + c * a.ldqt + r, turn[col * 16 + (tc ^ (col >> 3))], a.rows - r);
         }
     }
 }
@@ -187,9 +187,6 @@ namespace {
 template <typename T, int kFormat>
 zr_status quantize_run(const QuantArgs &a, int32_t block_rows, hipStream_t st)
 {
-    const bool aligned = aligned_to(a.src, 16) && (a.ld % 8 == 0 || a.rows == 1) &&
-                         (!a.q || (aligned_to(a.q, 8) && (a.ldq % 8 == 0 || a.rows == 1))) &&
-                         (!a.qt || (aligned_to(a.qt, 8) && (a.ldqt % 8 == 0 || a.cols == 1)));
     if (block_rows == 1 && !a.qt) {
         QuantArgs f = a;
         // rows without gaps whose groups are whole are one long row
@@ -200,16 +197,12 @@ zr_status quantize_run(const QuantArgs &a, int32_t block_rows, hipStream_t st)
         }
         const int64_t groups = f.rows * f.gc;
         const dim3 grid = grid_of((groups + kBlock / 16 - 1) / (kBlock / 16));
-        return aligned ? launch(quantize_rows_kernel<T, kFormat, true>, grid, dim3(kBlock), 0, st, f, groups)
-                       : launch(quantize_rows_kernel<T, kFormat, false>, grid, dim3(kBlock), 0, st, f, groups);
+        return launch(quantize_rows_kernel<T, kFormat>, grid, dim3(kBlock), 0, st, f, groups);
     }
     const int64_t tiles = a.gr * a.gc;
     const dim3 grid = grid_of(tiles);
-    if (block_rows == 1)
-        return aligned ? launch(quantize_tile_kernel<T, kFormat, false, true>, grid, dim3(kBlock), 0, st, a, tiles)
-                       : launch(quantize_tile_kernel<T, kFormat, false, false>, grid, dim3(kBlock), 0, st, a, tiles);
-    return aligned ? launch(quantize_tile_kernel<T, kFormat, true, true>, grid, dim3(kBlock), 0, st, a, tiles)
-                   : launch(quantize_tile_kernel<T, kFormat, true, false>, grid, dim3(kBlock), 0, st, a, tiles);
+    return block_rows == 1 ? launch(quantize_tile_kernel<T, kFormat, false>, grid, dim3(kBlock), 0, st, a, tiles)
+                           : launch(quantize_tile_kernel<T, kFormat, true>, grid, dim3(kBlock), 0, st, a, tiles);
 }
 
 }  // namespace

@@ -7,8 +7,8 @@
 // + dh and dweight = sum over rows of dy * xh.
 //
 // Sums are fp32: a lane's elements in column order, then the lanes of a wave and
-// the waves of a row in a fixed tree, so results depend only on the inputs and on
-// whether every row starts on 16 bytes, not on the grid.  Both passes are bound by HBM.
+// the waves of a row in a fixed tree, so results depend only on the inputs, not
+// on the grid or on addresses.  Both passes are bound by HBM.
 #include "fp8.hpp"
 
 namespace zr {
@@ -54,7 +54,7 @@ __device__ __forceinline__ float rstd_of(float sum, int64_t cols, float eps)
 
 // y, codes and scales of eight columns from c on (n of them inside the row),
 // held by a lane of the row of 16 lanes that holds the group.
-template <typename T, bool kAligned>
+template <typename T>
 __device__ __forceinline__ void norm_outputs(const NormArgs &a, int64_t row, int64_t c, int64_t n, u32x4 h, u32x4 w,
                                              float rstd)
 {
@@ -69,7 +69,7 @@ __device__ __forceinline__ void norm_outputs(const NormArgs &a, int64_t row, int
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             o[i] = T::pack(y[2 * i], y[2 * i + 1]);
-        store8<kAligned, true>(a.y + row * a.ldy + c, o, n);
+        store8<true>(a.y + row * a.ldy + c, o, n);
     }
     if (a.q) {
         uint32_t amax = 0;
@@ -78,7 +78,7 @@ __device__ __forceinline__ void norm_outputs(const NormArgs &a, int64_t row, int
             amax = max_u32(amax, __float_as_uint(y[e]) & 0x7fffffffu);
         const uint32_t s = scale_byte<ZR_E4M3>(group_max(amax));
         const float inv = inverse_scale(s);
-        store_codes8<kAligned>(a.q + row * a.ldq + c,
+        store_codes8(a.q + row * a.ldq + c,
                                u32x2{codes4<ZR_E4M3>(y[0], y[1], y[2], y[3], inv, s),
                                      codes4<ZR_E4M3>(y[4], y[5], y[6], y[7], inv, s)}, n);
         if ((threadIdx.x & 15) == 0 && n > 0)
@@ -96,10 +96,9 @@ __device__ __forceinline__ float block_sum(float v, float (*part)[4], int slot)
     return (part[slot][0] + part[slot][1]) + (part[slot][2] + part[slot][3]);
 }
 
-// Rows of any length and alignment: a workgroup per row, read twice (the second
-// time from cache).  h is written in the second read, so that it may replace x
-// or residual.  16384 x 4096 with residual, h, y and codes: 122 us.
-template <typename T, bool kAligned>
+// Rows of any length: a workgroup per row, read twice (the second time from cache).  h is written in the second read, so that it may replace x
+// or residual.  16384 x 4096 with residual, h, y and codes takes 122 us so.
+template <typename T>
 __global__ __launch_bounds__(kBlock) void norm_wide_kernel(NormArgs a)
 {
     __shared__ float part[2][4];
@@ -108,9 +107,9 @@ __global__ __launch_bounds__(kBlock) void norm_wide_kernel(NormArgs a)
         const uint16_t *x = a.x + row * a.ldx, *r = a.residual ? a.residual + row * a.ldr : nullptr;
         float sum = 0.0f;
         for (int64_t c = threadIdx.x * kVec; c < a.cols; c += kBlock * kVec) {
-            u32x4 h = load8<kAligned>(x + c, a.cols - c);
+            u32x4 h = load8(x + c, a.cols - c);
             if (r)
-                h = stream8<T>(h, load8<kAligned>(r + c, a.cols - c));
+                h = stream8<T>(h, load8(r + c, a.cols - c));
             sum = squares8<T>(h, sum);
         }
         const float rstd = rstd_of(block_sum(wave_sum(sum), part, slot), a.cols, a.eps);
@@ -119,12 +118,12 @@ __global__ __launch_bounds__(kBlock) void norm_wide_kernel(NormArgs a)
         // whole rows of 16 lanes stay in the loop: they share a group's maximum
         for (int64_t c = threadIdx.x * kVec; c - (threadIdx.x & 15) * kVec < a.cols; c += kBlock * kVec) {
             const int64_t n = a.cols - c;
-            u32x4 h = load8<kAligned>(x + c, n);
+            u32x4 h = load8(x + c, n);
             if (r)
-                h = stream8<T>(h, load8<kAligned>(r + c, n));
+                h = stream8<T>(h, load8(r + c, n));
             if (a.h)
-                store8<kAligned, true>(a.h + row * a.ldh + c, h, n);
-            norm_outputs<T, kAligned>(a, row, c, n, h, load8<kAligned>(a.weight + c, n), rstd);
+                store8<true>(a.h + row * a.ldh + c, h, n);
+            norm_outputs<T>(a, row, c, n, h, load8(a.weight + c, n), rstd);
         }
     }
 }
@@ -150,20 +149,20 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : kBlock) void norm_row_ke
         for (int v = 0; v < NV; ++v) {
             const int32_t c = ((v * kWaves + w0) * 64 + lane) * kVec;
             n[v] = live ? (int32_t)a.cols - c : 0;
-            h[v] = load8<true>(a.x + row * a.ldx + c, n[v]);
+            h[v] = load8(a.x + row * a.ldx + c, n[v]);
         }
         if (a.residual) {
             u32x4 r[NV];
 #pragma unroll
             for (int v = 0; v < NV; ++v)
-                r[v] = load8<true>(a.residual + row * a.ldr + ((v * kWaves + w0) * 64 + lane) * kVec, n[v]);
+                r[v] = load8(a.residual + row * a.ldr + ((v * kWaves + w0) * 64 + lane) * kVec, n[v]);
 #pragma unroll
             for (int v = 0; v < NV; ++v)
                 h[v] = stream8<T>(h[v], r[v]);
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            w[v] = load8<true>(a.weight + ((v * kWaves + w0) * 64 + lane) * kVec, n[v]);
+            w[v] = load8(a.weight + ((v * kWaves + w0) * 64 + lane) * kVec, n[v]);
         float sum = 0.0f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
@@ -185,8 +184,8 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : kBlock) void norm_row_ke
         for (int v = 0; v < NV; ++v) {
             const int64_t c = ((v * kWaves + w0) * 64 + lane) * kVec;
             if (a.h)
-                store8<true, true>(a.h + row * a.ldh + c, h[v], n[v]);
-            norm_outputs<T, true>(a, row, c, n[v], h[v], w[v], rstd);
+                store8<true>(a.h + row * a.ldh + c, h[v], n[v]);
+            norm_outputs<T>(a, row, c, n[v], h[v], w[v], rstd);
         }
     }
 }
@@ -233,9 +232,9 @@ __device__ __forceinline__ float dx_factor(float dot, float rstd, int64_t cols)
     return __fdiv_rn(dot, (float)cols) * rstd * rstd;
 }
 
-// dx for rows of any length and alignment, read twice.  With the partial sums of the
-// weight gradient, which read dy and h once more by columns, 16384 x 4096 takes 383 us.
-template <typename T, bool kAligned>
+// dx for rows of any length, read twice.  With the partial sums of the
+// weight gradient, which read dy and h once more by columns, 16384 x 4096 takes 383 us so.
+template <typename T>
 __global__ __launch_bounds__(kBlock) void norm_dx_wide_kernel(NormGradArgs a)
 {
     __shared__ float part[2][4];
@@ -244,16 +243,16 @@ __global__ __launch_bounds__(kBlock) void norm_dx_wide_kernel(NormGradArgs a)
         const uint16_t *dy = a.dy + row * a.lddy, *h = a.h + row * a.ldh;
         float sum = 0.0f;
         for (int64_t c = threadIdx.x * kVec; c < a.cols; c += kBlock * kVec)
-            sum = dots8<T>(load8<kAligned>(dy + c, a.cols - c), load8<kAligned>(a.weight + c, a.cols - c),
-                           load8<kAligned>(h + c, a.cols - c), sum);
+            sum = dots8<T>(load8(dy + c, a.cols - c), load8(a.weight + c, a.cols - c),
+                           load8(h + c, a.cols - c), sum);
         const float rstd = a.rstd[row];
         const float k = dx_factor(block_sum(wave_sum(sum), part, slot), rstd, a.cols);
         for (int64_t c = threadIdx.x * kVec; c < a.cols; c += kBlock * kVec) {
             const int64_t n = a.cols - c;
-            const u32x4 dh = a.dh ? load8<kAligned>(a.dh + row * a.lddh + c, n) : u32x4{0, 0, 0, 0};
-            store8<kAligned, true>(a.dx + row * a.lddx + c,
-                             dx8<T>(load8<kAligned>(dy + c, n), load8<kAligned>(a.weight + c, n),
-                                    load8<kAligned>(h + c, n), dh, rstd, k), n);
+            const u32x4 dh = a.dh ? load8(a.dh + row * a.lddh + c, n) : u32x4{0, 0, 0, 0};
+            store8<true>(a.dx + row * a.lddx + c,
+                             dx8<T>(load8(dy + c, n), load8(a.weight + c, n),
+                                    load8(h + c, n), dh, rstd, k), n);
         }
     }
 }
@@ -297,7 +296,7 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad_row_kernel(NormGradArg
     for (int v = 0; v < NV; ++v) {
         c[v] = ((v * kWaves + w0) * 64 + lane) * kVec;
         n[v] = (int32_t)a.cols - c[v];
-        w[v] = load8<true>(a.weight + c[v], n[v]);
+        w[v] = load8(a.weight + c[v], n[v]);
     }
     const int64_t stride = a.parts * kSlots;
     for (int64_t p = blockIdx.x; p < a.parts; p += gridDim.x) {
@@ -311,9 +310,9 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad_row_kernel(NormGradArg
             const bool live = row < a.rows;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                dy[v] = load8<true>(a.dy + row * a.lddy + c[v], live ? n[v] : 0);
-                h[v] = load8<true>(a.h + row * a.ldh + c[v], live ? n[v] : 0);
-                dh[v] = a.dh ? load8<true>(a.dh + row * a.lddh + c[v], live ? n[v] : 0) : u32x4{0, 0, 0, 0};
+                dy[v] = load8(a.dy + row * a.lddy + c[v], live ? n[v] : 0);
+                h[v] = load8(a.h + row * a.ldh + c[v], live ? n[v] : 0);
+                dh[v] = a.dh ? load8(a.dh + row * a.lddh + c[v], live ? n[v] : 0) : u32x4{0, 0, 0, 0};
             }
             rstd = live ? a.rstd[row] : 0.0f;
         };
@@ -356,7 +355,7 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad_row_kernel(NormGradArg
                     d[1] = __builtin_fmaf(T::hi(o_dy[v][i]), T::hi(o_h[v][i]) * r, d[1]);
                 }
                 if (row < a.rows)
-                    store8<true, true>(a.dx + row * a.lddx + c[v], dx8<T>(o_dy[v], w[v], o_h[v], o_dh[v], r, k), n[v]);
+                    store8<true>(a.dx + row * a.lddx + c[v], dx8<T>(o_dy[v], w[v], o_h[v], o_dh[v], r, k), n[v]);
             }
             if constexpr (!kEarly)
                 load(row + stride);
@@ -428,11 +427,8 @@ zr_status norm_rows(const NormArgs &a, hipStream_t st)
 // row; longer rows take four, and from 16385 columns on a row no longer fits the registers
 // of 8 waves.
 template <typename T>
-zr_status norm_run(const NormArgs &a, bool aligned, hipStream_t st)
+zr_status norm_run(const NormArgs &a, hipStream_t st)
 {
-    const dim3 grid = grid_of(a.rows);
-    if (!aligned)
-        return launch(norm_wide_kernel<T, false>, grid, dim3(kBlock), 0, st, a);
     if (a.cols <= 512)
         return norm_rows<T, 1, 1>(a, st);
     if (a.cols <= 1024)
@@ -445,7 +441,7 @@ zr_status norm_run(const NormArgs &a, bool aligned, hipStream_t st)
         return norm_rows<T, 2, 8>(a, st);
     if (a.cols <= 16384)
         return norm_rows<T, 4, 8>(a, st);
-    return launch(norm_wide_kernel<T, true>, grid, dim3(kBlock), 0, st, a);
+    return launch(norm_wide_kernel<T>, grid_of(a.rows), dim3(kBlock), 0, st, a);
 }
 
 template <typename T, int NV, int kWaves>
@@ -459,9 +455,9 @@ zr_status norm_grad_rows(NormGradArgs a, hipStream_t st)
 }
 
 template <typename T>
-zr_status norm_backward_run(NormGradArgs a, bool aligned, hipStream_t st)
+zr_status norm_backward_run(NormGradArgs a, hipStream_t st)
 {
-    if (a.rows > 0 && aligned && a.cols <= 16384) {
+    if (a.rows > 0 && a.cols <= 16384) {
         if (a.cols <= 512)
             return norm_grad_rows<T, 1, 1>(a, st);
         if (a.cols <= 1024)
@@ -481,14 +477,10 @@ zr_status norm_backward_run(NormGradArgs a, bool aligned, hipStream_t st)
         const int64_t blocks = (a.cols + kBlock - 1) / kBlock * a.parts;
         s = launch(norm_dweight_partial_kernel<T>, grid_of(blocks), dim3(kBlock), 0, st, a);
         if (s == ZR_OK)
-            s = aligned ? launch(norm_dx_wide_kernel<T, true>, grid_of(a.rows), dim3(kBlock), 0, st, a)
-                        : launch(norm_dx_wide_kernel<T, false>, grid_of(a.rows), dim3(kBlock), 0, st, a);
+            s = launch(norm_dx_wide_kernel<T>, grid_of(a.rows), dim3(kBlock), 0, st, a);
     }
     return s != ZR_OK ? s : launch(norm_dweight_kernel<T>, grid_of((a.cols + 31) / 32), dim3(kGradThreads), 0, st, a);
 }
-
-// A matrix of 16-bit elements on 16-byte boundaries in every row.
-bool rows_aligned(const void *p, int64_t ld, int64_t rows) { return !p || (aligned_to(p, 16) && (ld % kVec == 0 || rows <= 1)); }
 
 bool same_matrix(const void *p, int64_t ldp, const void *q, int64_t ldq) { return p == q && ldp == ldq; }
 
@@ -541,11 +533,8 @@ extern "C" zr_status zr_rmsnorm_fp8(const void *x, int64_t ldx, const void *resi
     const NormArgs a{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(residual),
                      static_cast<const uint16_t *>(weight), ldx, ldr, rows, cols, (float)eps,
                      static_cast<uint16_t *>(h), static_cast<uint16_t *>(y), ldh, ldy, q, scales, ldq, rstd};
-    const bool aligned = rows_aligned(x, ldx, rows) && rows_aligned(residual, ldr, rows) && aligned_to(weight, 16) &&
-                         rows_aligned(h, ldh, rows) && rows_aligned(y, ldy, rows) &&
-                         (!q || (aligned_to(q, 8) && (ldq % 8 == 0 || rows == 1)));
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return dtype == ZR_BF16 ? norm_run<BF16>(a, aligned, st) : norm_run<F16>(a, aligned, st);
+    return dtype == ZR_BF16 ? norm_run<BF16>(a, st) : norm_run<F16>(a, st);
 }
 
 extern "C" zr_status zr_rmsnorm_backward(const void *dy, int64_t lddy, const void *h, int64_t ldh, const void *weight,
@@ -585,8 +574,6 @@ extern "C" zr_status zr_rmsnorm_backward(const void *dy, int64_t lddy, const voi
                          static_cast<const uint16_t *>(weight), static_cast<const uint16_t *>(dh), rstd, lddy, ldh,
                          lddh, rows, cols, static_cast<uint16_t *>(dx), static_cast<uint16_t *>(dweight), lddx,
                          workspace, 0};
-    const bool aligned = rows_aligned(dy, lddy, rows) && rows_aligned(h, ldh, rows) && aligned_to(weight, 16) &&
-                         rows_aligned(dh, lddh, rows) && rows_aligned(dx, lddx, rows);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return dtype == ZR_BF16 ? norm_backward_run<BF16>(a, aligned, st) : norm_backward_run<F16>(a, aligned, st);
+    return dtype == ZR_BF16 ? norm_backward_run<BF16>(a, st) : norm_backward_run<F16>(a, st);
 }
