@@ -27,6 +27,7 @@
 namespace zr {
 
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef float any_f32x4 __attribute__((ext_vector_type(4), aligned(4)));
 
 struct MatmulArgs {
     const uint8_t *a, *b, *sa, *sb;
@@ -35,7 +36,6 @@ struct MatmulArgs {
     void *out;
     int64_t ldo;
     int32_t dtype, accumulate;
-    int32_t whole;  // rows of out start on 16-byte boundaries
 };
 
 constexpr int kCus = 256;             // compute units
@@ -60,13 +60,13 @@ __device__ __forceinline__ u32x2 add4(u32x2 old, f32x4 v, bool accumulate)
 __device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_t j, f32x4 v, int64_t n)
 {
     const int64_t at = i * p.ldo + j;
-    const bool vec = p.whole && n >= kAccum;
+    const bool vec = n >= kAccum;  // at any address
     if (p.dtype == ZR_F32) {
         float *o = static_cast<float *>(p.out) + at;
         if (p.accumulate) {
             f32x4 old = {0.0f, 0.0f, 0.0f, 0.0f};
             if (vec) {
-                old = *(global_ptr<const f32x4>)o;
+                old = *(global_ptr<const any_f32x4>)o;
             } else {
 #pragma unroll
                 for (int e = 0; e < kAccum; ++e)
@@ -77,7 +77,7 @@ __device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_
             v += old;
         }
         if (vec) {
-            *(global_ptr<f32x4>)o = v;
+            *(global_ptr<any_f32x4>)o = v;
             return;
         }
 #pragma unroll
@@ -90,7 +90,7 @@ __device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_
     u32x2 w = {0, 0};
     if (p.accumulate) {
         if (vec) {
-            w = *(global_ptr<const u32x2>)o;
+            w = *(global_ptr<const any_u32x2>)o;
         } else {
 #pragma unroll
             for (int e = 0; e < kAccum; ++e)
@@ -101,7 +101,7 @@ __device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_
     }
     w = p.dtype == ZR_BF16 ? add4<BF16>(w, v, p.accumulate) : add4<F16>(w, v, p.accumulate);
     if (vec) {
-        *(global_ptr<u32x2>)o = w;
+        *(global_ptr<any_u32x2>)o = w;
         return;
     }
 #pragma unroll
@@ -116,7 +116,7 @@ __device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_
     uint16_t *o = static_cast<uint16_t *>(p.out) + i * p.ldo + j;
     u32x4 w = {0, 0, 0, 0};
     if (p.accumulate) {
-        w = p.whole ? load8<true>(o, n) : load8<false>(o, n);
+        w = load8(o, n);
         __builtin_amdgcn_s_waitcnt(kWaitLoads);
     }
     const u32x2 a = {w[0], w[1]}, b = {w[2], w[3]};
@@ -129,10 +129,7 @@ __device__ __forceinline__ void store_out(const MatmulArgs &p, int64_t i, int64_
         d = add4<F16>(b, hi, p.accumulate);
     }
     w = u32x4{c[0], c[1], d[0], d[1]};
-    if (p.whole)
-        store8<true>(o, w, n);
-    else
-        store8<false>(o, w, n);
+    store8(o, w, n);
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -385,12 +382,16 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // next is loaded, and workgroups stay for several tiles, so that a tile's first loads fall
 // under the last products of the one before.
 //
-// Bound by power: with random codes the matrix unit alone, fed from registers, reaches 4.0
-// PFLOP/s of the 4.95 that it reaches with zeros, and with the loads beside it the clock
-// falls further, to 1.7 to 2.0 GHz.  16384 x 11008 x 4096: 632 us, 2.34 PFLOP/s; 16384 cubed
-// 2.6 PFLOP/s; 11008 x 4096 x 8111 (e5m2) 320 us.  Measured and not kept: 16 x 16 x 128
-// instructions (682 us at a state of 655), scales read as bytes so that nothing waits at mid-group (1.5 to
-// 3 % slower), results packed before they are turned (spills).
+// 16384 x 11008 x 4096: 632 us, 2.34 PFLOP/s; 16384 cubed 2.6 PFLOP/s; 11008 x 4096 x 8111
+// (e5m2) 316 us.  A group takes 1.55 us, 0.85 of them products at full clock.  Power is one
+// bound: with zeros for codes a group takes 1.2 us, with random ones the clock falls to 1.9
+// GHz (the matrix unit alone, fed from registers, reaches 4.95 and 4.0 PFLOP/s).  Issue is the
+// other: without loads, reads of LDS and scales the same loop reaches 3.8.  A tile's end
+// takes 9.5 us, in which all workgroups store 33 MB at once.  Measured and not kept: 16 x 16 x
+// 128 instructions (682 us at a state of 655), scales read as bytes so that nothing waits at
+// mid-group (1.5 to 3 % slower), results packed before they are turned (spills), loads by half
+// groups, which gives them twice the time but makes twice the requests (700 us), and no wait
+// for a tile's stores in the next one's first group (1 % slower).
 constexpr int kBig = 256;                    // output rows and columns of a workgroup
 constexpr int kOperandStage = kBig * kGroup;  // LDS bytes of one group of one operand
 constexpr int kStage = 2 * kOperandStage;
@@ -1292,7 +1293,7 @@ extern "C" zr_status zr_matmul_fp8(const uint8_t *a, int64_t lda, const uint8_t 
                 return fail(ZR_EINVAL, "%s: out overlaps another buffer", who);
     }
     const MatmulArgs p{a, b, a_scales, b_scales, lda, ldb, m, n, k, kb, b_block_rows == 1 ? 0 : 7, out, ldo,
-                       out_dtype, accumulate, aligned_to(out, 16) && (ldo * size % 16 == 0 || m == 1)};
+                       out_dtype, accumulate};
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (out_dtype == ZR_F32)
         return a_format == ZR_E4M3 ? matmul_run<ZR_E4M3, true>(p, st) : matmul_run<ZR_E5M2, true>(p, st);
