@@ -219,3 +219,39 @@ def test_capture_refuses_what_eager_refuses():
     zr.zr_graph_launch(gr, stream)
     stream.synchronize()
     assert bool((s.view(torch.uint8) == 0).all())
+
+
+def test_one_tensor_twice():
+    """Inputs may be one tensor: x as its own residual, a matrix times its own transpose, the
+    stream's gradient that is also the norm's."""
+    device()
+    x, _, w, _, _ = layer(130, 128, 516, 5)
+    outs = []
+    for twin in (x, x.clone()):
+        y, h, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(130, device="cuda")
+        q, s = zr.fp8_matrix(130, 516)
+        zr.zr_rmsnorm_fp8(x, w, y, residual=twin, h=h, rstd=rstd)
+        zr.zr_quantize_fp8(y, q, s)
+        q2, s2 = (q, s) if twin is x else (q.clone(), s.clone())
+        gram = torch.empty(130, 130, device="cuda")
+        zr.zr_matmul_fp8(q, s, q2, s2, gram)
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        zr.zr_rmsnorm_backward(y, h, w, rstd, dx, dw, zr.rmsnorm_workspace(516), dh=y if twin is x else y.clone())
+        outs.append([y, h, rstd, gram, dx, dw])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert torch.equal(outs[0][3], outs[0][3].t())
+
+
+def test_views_of_one_buffer():
+    """Operands and results that are pieces of one allocation, at odd addresses, side by side."""
+    device()
+    raw = torch.full((3 * 70 * 301 + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    pieces = [raw[1 + i * 70 * 301:1 + (i + 1) * 70 * 301].view(70, 301) for i in range(3)]
+    x, res, w, _, _ = layer(70, 128, 301, 6)
+    pieces[0].copy_(x)
+    pieces[1].copy_(res)
+    y = torch.empty_like(x)
+    zr.zr_rmsnorm_fp8(x, w, y, residual=res)
+    zr.zr_rmsnorm_fp8(pieces[0], w, pieces[2], residual=pieces[1])
+    assert torch.equal(pieces[2], y) and torch.equal(pieces[0], x) and torch.equal(pieces[1], res)
+    assert bool(raw[0].isnan()) and bool(raw[1 + 3 * 70 * 301:].isnan().all())

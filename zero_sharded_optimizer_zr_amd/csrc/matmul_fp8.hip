@@ -525,7 +525,7 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
             if (split) {
                 const uint32_t last_a = (bytes_a - 1) & ~3u, last_b = (bytes_b - 1) & ~3u;
                 load4_to_lds(rsa, xa < last_a ? xa + 4 : last_a, to + 1024);
-                load4_to_lds(rsb, xb < last_b ? xb + 4 : last_b, to + 3072);
+                load4_to_lds(rsb, xb < last_b ? xb + 4 : last_b, to + 3 * 1024);
             }
             load_words ^= kScaleBlock;
         }
