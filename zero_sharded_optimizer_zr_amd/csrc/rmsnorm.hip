@@ -299,6 +299,9 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad_row_kernel(NormGradArg
         w[v] = load8(a.weight + c[v], n[v]);
     }
     const int64_t stride = a.parts * kSlots;
+    // alternates over all rounds, also from one group of rows to the next: where a row takes the
+    // whole workgroup the barrier of a sum is the only one there is
+    int flip = 0;
     for (int64_t p = blockIdx.x; p < a.parts; p += gridDim.x) {
         f32x4 dw[NV][2];
 #pragma unroll
@@ -316,7 +319,6 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad_row_kernel(NormGradArg
             }
             rstd = live ? a.rstd[row] : 0.0f;
         };
-        int flip = 0;
         // the same number of rounds in every slot
         load(p * kSlots + slot);
         for (int64_t row0 = p * kSlots; row0 < a.rows; row0 += stride, flip ^= 1) {
