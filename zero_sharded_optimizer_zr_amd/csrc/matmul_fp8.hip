@@ -16,8 +16,9 @@
 // fp32).  On normal data that leaves the sum 1.4e-5 off, a hundredth of a rounding
 // to bf16 and a tenth of one to fp16, so 16-bit outputs take that path.  An fp32
 // output would keep that error, so its codes are widened to bf16 (exact: at most 3
-// mantissa bits; the scale is applied by the conversion), whose products the matrix
-// unit adds in fp32 (7e-8 off), at half the rate.
+// mantissa bits; the scale is applied by the conversion, and elements past bf16's
+// range are taken smaller, see lower_scales), whose products the matrix unit adds in
+// fp32 (7e-8 off), at half the rate.
 //
 // Four kernels: waves that split the summed axis (few rows, any alignment), 128 x 64
 // outputs by two teams, 128 x 128 through a ring in LDS, and 256 x 256 for the large
@@ -156,6 +157,127 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi, float scale)
     return o;
 }
 
+// Elements past bf16's range.  A scale byte from kFar on (247 for e4m3, 240 for e5m2; 255
+// is NaN) makes elements of 2^128 and more, which the widening would turn into infinities
+// although their products may be small: the largest bf16 value's own code is 2^128.
+// Where a group has such a scale, its row or column is widened 2^16 times smaller, and
+// the sums of that row or column are taken 2^16 times smaller over this group; all others
+// keep their bits.  Sums below 2^-90, which could lose bits, stay as they are: the products
+// they meet are zeros, and the sum is right without the factor, or multiples of 2^-52 (a
+// code of at least 2^-16 or 2^-9 times 2^(kFar - 16 - 127) times at least 2^-133), beside
+// which they are nothing (2^-38 of the result).  Looking for such scales, which are rare,
+// takes 1 to 3 % (11008 x 4096 x 8192 752 us at 739 without, 333 x 4096 x 4096 21.0 at 20.4).
+template <int kFormat>
+constexpr uint32_t kFar = kFormat == ZR_E4M3 ? 247 : 240;
+
+// The lowered scales of a lane's accumulators and the sums held as they are.
+struct Lowered {
+    uint32_t marks;  // a bit for accumulator e of column tile z at z * kAccum + e, for row tile y at 16 + y
+    uint64_t held;   // a bit for each accumulator
+};
+
+template <int kFormat>
+__device__ __forceinline__ bool is_far(uint32_t s)
+{
+    return s >= kFar<kFormat> && s < 255u;
+}
+
+// How often an accumulator is taken 2^16 times smaller: 0, 1 or 2.
+__device__ __forceinline__ int times(uint32_t marks, int y, int at)
+{
+    return (int)(marks >> at & 1) + (int)(marks >> (16 + y) & 1);
+}
+
+// One tile's sums after another, and back where the products take them (kPinned: in the
+// matrix unit's registers): few registers are free.
+template <bool kPinned>
+__device__ __forceinline__ void one_tile(f32x4 &v, Lowered &low)
+{
+    if constexpr (kPinned)
+        asm volatile("" : "+a"(v), "+v"(low.marks), "+v"(low.held));
+    else
+        asm volatile("" : "+v"(v), "+v"(low.marks), "+v"(low.held));
+}
+
+// Lowers the scales of a group, and the sums, where needed; false if nowhere.
+template <bool kPinned, int kFormatA, int MT, int NT>
+__device__ __forceinline__ bool lower_scales(uint32_t *ca, uint32_t *cb, f32x4 (&acc)[MT][NT], Lowered &low)
+{
+    // one maximum over both operands: the lower limit of the two, here, for either
+    uint32_t most = ca[0];
+#pragma unroll
+    for (int y = 1; y < MT; ++y)
+        most = max_u32(most, ca[y]);
+#pragma unroll
+    for (int z = 0; z < NT; ++z)
+        most = max_u32(most, cb[z]);
+    if (!__any(most >= kFar<kFormatA>))
+        return false;
+    low = {0, 0};
+#pragma unroll
+    for (int y = 0; y < MT; ++y) {
+        const bool far = is_far<kFormatA>(ca[y]);
+        low.marks |= (uint32_t)far << (16 + y);
+        ca[y] -= far ? 16 : 0;
+    }
+    // this lane has the scale of one row of B in each tile, and accumulators of four
+#pragma unroll
+    for (int z = 0; z < NT; ++z) {
+        const bool far = is_far<ZR_E4M3>(cb[z]);
+        const uint64_t lanes = __ballot(far);
+        low.marks |= (uint32_t)(lanes >> ((threadIdx.x & 63) / 16 * kAccum) & 15) << (z * kAccum);
+        cb[z] -= far ? 16 : 0;
+    }
+#pragma unroll
+    for (int y = 0; y < MT; ++y)
+#pragma unroll
+        for (int z = 0; z < NT; ++z) {
+            f32x4 v = acc[y][z];
+            one_tile<kPinned>(v, low);
+#pragma unroll
+            for (int e = 0; e < kAccum; ++e) {
+                const bool hold = !(__builtin_fabsf(v[e]) >= 0x1p-90f);
+                v[e] = __builtin_ldexpf(v[e], hold ? 0 : -16 * times(low.marks, y, z * kAccum + e));
+                low.held |= (uint64_t)hold << ((y * NT + z) * kAccum + e);
+            }
+            one_tile<kPinned>(v, low);
+            acc[y][z] = v;
+        }
+    return true;
+}
+
+// Sums stay in the matrix unit's registers where paths meet.
+template <int MT, int NT>
+__device__ __forceinline__ void pin(f32x4 (&acc)[MT][NT])
+{
+#pragma unroll
+    for (int y = 0; y < MT; ++y)
+#pragma unroll
+        for (int z = 0; z < NT; ++z)
+            asm volatile("" : "+a"(acc[y][z]));
+}
+
+// After the group's products.
+template <bool kPinned, int MT, int NT>
+__device__ __forceinline__ void raise_sums(f32x4 (&acc)[MT][NT], Lowered &low)
+{
+#pragma unroll
+    for (int y = 0; y < MT; ++y)
+#pragma unroll
+        for (int z = 0; z < NT; ++z) {
+            f32x4 v = acc[y][z];
+            one_tile<kPinned>(v, low);
+#pragma unroll
+            for (int e = 0; e < kAccum; ++e) {
+                // no product came to a held sum that is still small
+                const bool alone = (low.held >> ((y * NT + z) * kAccum + e) & 1) && __builtin_fabsf(v[e]) < 0x1p-60f;
+                v[e] = __builtin_ldexpf(v[e], alone ? 0 : 16 * times(low.marks, y, z * kAccum + e));
+            }
+            one_tile<kPinned>(v, low);
+            acc[y][z] = v;
+        }
+}
+
 // A lane's 32 codes of an operand from two 16-byte pieces.
 __device__ __forceinline__ i32x8 operand(u32x4 lo, u32x4 hi)
 {
@@ -230,6 +352,8 @@ __device__ __forceinline__ void multiply_group(const SplitGroup<MT, NT> &s, f32x
                     operand(s.b[z][0], s.b[z][1]), operand(s.a[y][0], s.a[y][1]), acc[y][z], ZR_E4M3, kFormatA, 0,
                     (int)cb[z], 0, (int)ca[y]);
     } else {
+        Lowered low;
+        const bool far = lower_scales<false, kFormatA>(ca, cb, acc, low);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // 8 codes of each lane at a time
             const int h = i / 2, e = i % 2 * 2;
@@ -245,6 +369,8 @@ __device__ __forceinline__ void multiply_group(const SplitGroup<MT, NT> &s, f32x
                     acc[y][z] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[z], a, acc[y][z], 0, 0, 0);
             }
         }
+        if (far)
+            raise_sums<false>(acc, low);
     }
 }
 
@@ -877,6 +1003,10 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
             }
         }
         bf16x8 b[4], a;
+        Lowered low;
+        bool far = false;
+        if constexpr (kWide)
+            far = lower_scales<true, kFormatA>(ca[e], cb[e], acc, low);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             if constexpr (!kWide) {
@@ -906,6 +1036,11 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
                 load_piece(stage, i - 8);
             }
             __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (kWide) {
+            if (far)
+                raise_sums<true>(acc, low);
+            pin(acc);
         }
         load_done();
         // two stages on has landed, in every wave, and the next one has been read by all
@@ -1094,6 +1229,10 @@ __global__ __launch_bounds__(kPairThreads, 2) void matmul_pair_kernel(MatmulArgs
             const uint32_t next = stage == (kPairRing - 1) * kPairStage ? 0 : stage + kPairStage;
             constexpr int kParts = kWide ? 16 : 8, kHalf = kParts / 2;
             bf16x8 b[2], a;
+            Lowered low;
+            bool far = false;
+            if constexpr (kWide)
+                far = lower_scales<true, kFormatA>(ca[e], cb[e], acc, low);
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
                 if constexpr (!kWide) {
@@ -1129,6 +1268,11 @@ __global__ __launch_bounds__(kPairThreads, 2) void matmul_pair_kernel(MatmulArgs
                 for (int x = i * 6 / kParts; x < (i + 1) * 6 / kParts; ++x)
                     read_scale(e ^ 1, x, g + 1);
                 __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (kWide) {
+                if (far)
+                    raise_sums<true>(acc, low);
+                pin(acc);
             }
             // two stages on has landed, in every wave, and the next one has been read by all
             asm volatile("" ::: "memory");
