@@ -184,6 +184,15 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
                                                                   __builtin_bit_cast(u16x2, b)));
 }
 
+// Byte offset of group g (of kb) of a row of codes that starts at byte `row`, for a load
+// through a buffer descriptor; kNowhere, which is past the end of every buffer, for
+// groups behind the row and for lanes whose row is kNowhere.
+constexpr uint32_t kNowhere = 0xffffffffu;
+__host__ __device__ __forceinline__ uint32_t group_of_row(uint32_t row, int32_t g, int32_t kb)
+{
+    return row != kNowhere && g < kb ? row + (uint32_t)g * kGroup : kNowhere;
+}
+
 // Host side: *bytes = address range of a matrix of `size`-byte elements, from its
 // first to its last element (rows, cols > 0).  False if ld < cols or the range
 // does not fit int64.

@@ -633,7 +633,7 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
         ob = big_operand(p.b, p.ldb, p.n, p.k, j0, p.b_shift);
         // a quarter of the rows of each operand: neighbouring tiles share the rest
         const int quarter = (int)((wave < 2 ? j0 : i0) / kBig & 3) * 64 + (wave & 1) * 32 + lane;
-        ahead = lane < 32 ? row_at(quarter, wave < 2 ? oa.here : ob.here, wave < 2 ? p.lda : p.ldb) : 0xffffffffu;
+        ahead = lane < 32 ? row_at(quarter, wave < 2 ? oa.here : ob.here, wave < 2 ? p.lda : p.ldb) : kNowhere;
     };
     const auto load_piece = [&](uint32_t stage, int j) {  // j-th of 16 pieces of this wave
         const BigOperand &o = j & 1 ? oa : ob;
@@ -668,7 +668,7 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
     const auto prefetch = [&]() {
         constexpr int32_t kAhead = 1;
         const int32_t g = load_g + kAhead;
-        load4_to_lds(wave < 2 ? oa.rsrc : ob.rsrc, g < kb ? ahead + (uint32_t)g * kGroup : 0xffffffffu, dump0);
+        load4_to_lds(wave < 2 ? oa.rsrc : ob.rsrc, group_of_row(ahead, g, kb), dump0);
     };
     // zeros from code `tail` on in every row of a stage
     const auto clear_tail = [&](uint32_t at) {
