@@ -682,6 +682,20 @@ def _vector(t: Optional[torch.Tensor], dtypes, n: int, name: str) -> Optional[in
     return t.data_ptr() or None
 
 
+def _scales(t: Optional[torch.Tensor], rows: int, groups: int, name: str, exact: bool = False) -> Optional[int]:
+    """Address of the scales of `rows` rows (or blocks) of `groups` each: flat (one
+    dimension, or one row), or a matrix whose rows are of that length; with `exact`, of
+    as many rows."""
+    if t is not None and isinstance(t, torch.Tensor):
+        shape = t.shape
+        if shape == (rows, groups) and t.dtype in _SCALES and t.is_contiguous():  # the usual call, at less cost
+            return t.data_ptr() or None
+        if len(shape) == 2 and shape[0] > 1 and \
+                ((exact and shape[0] != rows) or (shape[1] != groups and (exact or rows > 1))):
+            raise ValueError(f"{name} is {shape[0]} x {shape[1]}, {rows} x {groups} needed")
+    return _vector(t, _SCALES, rows * groups, name)
+
+
 def _gpu_call_flat(fn, stream, tensors, *args) -> None:
     """_gpu_call for a flat tuple of tensors (or None), at less cost per call: these
     operators also run on single rows, where the call is longer than the kernel."""
@@ -732,8 +746,8 @@ def zr_quantize_fp8(src: torch.Tensor, q: Optional[torch.Tensor] = None, scales:
     if one is None:
         raise ValueError("neither q nor qt given")
     down, across = (rows, cols) if block_rows == 1 else (_groups(rows), _groups(cols))
-    p_s = _vector(scales, _SCALES, down * _groups(cols), "scales")
-    p_st = _vector(scales_t, _SCALES, across * _groups(rows), "scales_t")
+    p_s = _scales(scales, down, _groups(cols), "scales")
+    p_st = _scales(scales_t, across, _groups(rows), "scales_t")
     _gpu_call_flat(_lib.zr_quantize_fp8, stream, (src, q, scales, qt, scales_t), p_src, _DTYPES[src.dtype], rows,
                    cols, ld, int(block_rows), _FORMATS[one.dtype], p_q, ldq, p_s, p_qt, ldqt, p_st)
 
@@ -742,15 +756,16 @@ def zr_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sc
                   out: torch.Tensor, *, b_block_rows: int = 1, accumulate: bool = False, stream=None) -> None:
     """out [m, n] (bf16, fp16 or fp32) = A B^T for codes a [m, k] (e4m3 or e5m2) with a
     scale per 128 of a row and b [n, k] (e4m3) with a scale per 128 of a row
-    (b_block_rows 1) or per 128 x 128 block (128); accumulate adds to out."""
+    (b_block_rows 1) or per 128 x 128 block (128); accumulate adds to out.  Scales are
+    flat or matrices of their groups' shape."""
     (m, k), (n, kb) = _shape(a, "a"), _shape(b, "b")
     if k != kb:
         raise ValueError(f"a has rows of {k} codes, b of {kb}")
     p_a, lda = _matrix(a, _FORMATS, "a")
     p_b, ldb = _matrix(b, (torch.float8_e4m3fn,), "b")
     p_out, ldo = _matrix(out, _DTYPES, "out", (m, n))
-    p_sa = _vector(a_scales, _SCALES, m * _groups(k), "a_scales")
-    p_sb = _vector(b_scales, _SCALES, (n if b_block_rows == 1 else _groups(n)) * _groups(k), "b_scales")
+    p_sa = _scales(a_scales, m, _groups(k), "a_scales")
+    p_sb = _scales(b_scales, n if b_block_rows == 1 else _groups(n), _groups(k), "b_scales", exact=True)
     _gpu_call_flat(_lib.zr_matmul_fp8, stream, (a, a_scales, b, b_scales, out), p_a, lda, p_sa, _FORMATS[a.dtype],
                    p_b, ldb, p_sb, int(b_block_rows), m, n, k, p_out, _DTYPES[out.dtype], ldo,
                    int(bool(accumulate)))
@@ -773,7 +788,7 @@ def zr_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, y: Optional[torch.Tens
     p_y, ldy = _matrix(y, same, "y", shape)
     p_q, ldq = _matrix(q, (torch.float8_e4m3fn,), "q", shape)
     p_w = _vector(weight, same, cols, "weight")
-    p_s = _vector(scales, _SCALES, rows * _groups(cols), "scales")
+    p_s = _scales(scales, rows, _groups(cols), "scales")
     p_rstd = _vector(rstd, (torch.float32,), rows, "rstd")
     _gpu_call_flat(_lib.zr_rmsnorm_fp8, stream, (x, residual, weight, h, y, q, scales, rstd), p_x, ldx, p_r, ldr,
                    p_w, _DTYPES[x.dtype], rows, cols, float(eps), p_h, ldh, p_y, ldy, p_q, ldq, p_s, p_rstd)
