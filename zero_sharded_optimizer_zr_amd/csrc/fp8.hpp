@@ -57,12 +57,13 @@ __device__ __forceinline__ uint16_t narrow(float x)
 // an odd length need no path of their own (2961 x 402 normed in 6 us, with single
 // elements where rows do not start on 16 bytes 18; 16384 x 4095 in 171, 477; 2413 x 1915
 // quantized both ways in 18, 26).  kStream, here and below: the access carries the
-// non-temporal hint.
+// non-temporal hint (the builtins themselves: load_stream and store_stream would take the
+// vectors' full alignment for granted).
 template <bool kStream = false>
 __device__ __forceinline__ u32x4 load8(const uint16_t *p, int64_t n)
 {
     if (n >= kVec)
-        return kStream ? load_stream(reinterpret_cast<const any_u32x4 *>(p)) : *(global_ptr<const any_u32x4>)p;
+        return kStream ? __builtin_nontemporal_load((global_ptr<const any_u32x4>)p) : *(global_ptr<const any_u32x4>)p;
     u32x4 w = {0, 0, 0, 0};
 #pragma unroll
     for (int e = 0; e < kVec; ++e)
@@ -76,7 +77,7 @@ __device__ __forceinline__ void store8(uint16_t *p, u32x4 w, int64_t n)
 {
     if (n >= kVec) {
         if (kStream)
-            store_stream(reinterpret_cast<any_u32x4 *>(p), (any_u32x4)w);
+            __builtin_nontemporal_store((any_u32x4)w, (global_ptr<any_u32x4>)p);
         else
             *(global_ptr<any_u32x4>)p = w;
         return;
@@ -93,7 +94,7 @@ __device__ __forceinline__ void store_codes8(uint8_t *p, u32x2 w, int64_t n)
 {
     if (n >= kVec) {
         if (kStream)
-            store_stream(reinterpret_cast<any_u32x2 *>(p), (any_u32x2)w);
+            __builtin_nontemporal_store((any_u32x2)w, (global_ptr<any_u32x2>)p);
         else
             *(global_ptr<any_u32x2>)p = w;
         return;
