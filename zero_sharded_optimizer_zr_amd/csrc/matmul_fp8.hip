@@ -528,19 +528,24 @@ constexpr int kScaleBlock = 4 * kBig * 4;     // LDS bytes of four groups' scale
 __device__ __forceinline__ int staged(int row, int piece) { return row * kGroup + ((piece ^ (row >> 1 & 7)) << 4); }
 
 // 16 (or 4) bytes of each lane from `rsrc` at byte `at` + `k` into LDS from byte `to`
-// + `plus` (a constant) on, lane after lane.  No register is written; the caller waits on vmcnt.  In
-// assembly because the compiler would wait for every such load before any read of
-// the same LDS array, also of another stage.
+// + `plus` (a constant) on, lane after lane.  No vector register is written; the caller waits
+// on vmcnt.  In assembly because the compiler would wait for every such load before any
+// read of the same LDS array, also of another stage.  m0 holds the LDS address; the
+// compiler keeps it for itself (hence its warning), and sets it anew wherever it needs it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t at, int k, uint32_t to, int plus)
 {
     asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 :: "v"(at), "s"(rsrc), "s"(k), "s"(to), "i"(plus) : "scc");
+                 :: "v"(at), "s"(rsrc), "s"(k), "s"(to), "i"(plus) : "m0", "scc");
 }
 
 __device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t at, uint32_t to)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" :: "v"(at), "s"(rsrc), "s"(to));
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :: "v"(at), "s"(rsrc), "s"(to) : "m0");
 }
+#pragma clang diagnostic pop
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t *p, int64_t bytes)
 {
