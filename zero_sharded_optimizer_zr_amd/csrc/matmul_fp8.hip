@@ -1421,6 +1421,8 @@ extern "C" zr_status zr_matmul_fp8(const uint8_t *a, int64_t lda, const uint8_t 
         return fail(ZR_EINVAL, "%s: accumulate = %d, must be 0 or 1", who, accumulate);
     if (m < 0 || n < 0 || k < 0)
         return fail(ZR_EINVAL, "%s: negative size", who);
+    if (k > (int64_t)INT32_MAX * kGroup)
+        return fail(ZR_EINVAL, "%s: k = %lld is past 2^31 groups", who, (long long)k);
     if (m == 0 || n == 0 || (k == 0 && accumulate))
         return ZR_OK;
     const int64_t size = out_dtype == ZR_F32 ? 4 : 2;
