@@ -104,8 +104,8 @@ ZR_API zr_status zr_quantize_fp8(const void *src, zr_dtype dtype, int64_t rows, 
  * out may be a weight's piece of the flat gradient buffer (a contribution of
  * zr_reduce_slice); accumulate adds a further micro-batch.
  *
- * k == 0: out = 0 (unchanged with accumulate).  m or n == 0 is a no-op.  k is below
- * 2^31 groups.
+ * k == 0: out = 0 (unchanged with accumulate).  m or n == 0 is a no-op.  k is at most
+ * 2^31 - 65 groups.
  * Errors: ZR_EINVAL, ZR_EALIGN, ZR_EHIP.
  */
 ZR_API zr_status zr_matmul_fp8(const uint8_t *a, int64_t lda, const uint8_t *a_scales, zr_fp8_format a_format,

@@ -40,6 +40,8 @@ struct MatmulArgs {
 };
 
 constexpr int kCus = 256;             // compute units
+// Groups are counted in 32 bits, by a few at a time past the last one.
+constexpr int32_t kMostGroups = INT32_MAX - 64;
 constexpr int kWaitLoads = 0x0f70;   // s_waitcnt vmcnt(0)
 constexpr int kWaitAll = 0x0070;     // s_waitcnt vmcnt(0) lgkmcnt(0)
 constexpr int kWaitStage = 0x0071;   // s_waitcnt vmcnt(1) lgkmcnt(0)
@@ -1421,8 +1423,8 @@ extern "C" zr_status zr_matmul_fp8(const uint8_t *a, int64_t lda, const uint8_t 
         return fail(ZR_EINVAL, "%s: accumulate = %d, must be 0 or 1", who, accumulate);
     if (m < 0 || n < 0 || k < 0)
         return fail(ZR_EINVAL, "%s: negative size", who);
-    if (k > (int64_t)INT32_MAX * kGroup)
-        return fail(ZR_EINVAL, "%s: k = %lld is past 2^31 groups", who, (long long)k);
+    if (k > (int64_t)kMostGroups * kGroup)
+        return fail(ZR_EINVAL, "%s: k = %lld has too many groups", who, (long long)k);
     if (m == 0 || n == 0 || (k == 0 && accumulate))
         return ZR_OK;
     const int64_t size = out_dtype == ZR_F32 ? 4 : 2;
