@@ -32,7 +32,10 @@
  * allocation, capturable into a zr_graph.  Matrices are row-major; `ld` arguments
  * are the distance between rows in elements (>= the row length).  Buffers need
  * their element's natural alignment only; products of matrices of codes whose base
- * and row distance are multiples of 16 bytes are the fast ones.  The same call gives
+ * and row distance are multiples of 16 bytes are the fast ones.  zr_matmul_fp8 may read up
+ * to 15 bytes behind a matrix's last code, inside the aligned 16 bytes that hold it, and up to
+ * 3 on either side of an array of scales, inside aligned words; what is there does not
+ * count.  The same call gives
  * the same bits every time; the order of a product's fp32 sums, and with it their
  * last bit, goes by the call's sizes and by that alignment, never by the machine's
  * state.
@@ -93,9 +96,10 @@ ZR_API zr_status zr_quantize_fp8(const void *src, zr_dtype dtype, int64_t rows, 
  * ZR_F32; values past fp16's range become infinities).  With a 16-bit out the matrix
  * unit's 8-bit path adds each run of 8 products, aligned to the largest of them
  * with 13 bits below it, and the runs in fp32: on normal data 1.4e-5 of the result,
- * far below the rounding to 16 bits.  With ZR_F32 the codes are widened to bf16
- * and every addition is fp32, at half the rate; an element (code * scale) below
- * 2^-126 may count as 0 there.  A's codes are a_format, B's are e4m3.
+ * far below the rounding to 16 bits; sums that cancel keep the error of their terms.
+ * With ZR_F32 the codes are widened to bf16 and every addition is fp32, at half the
+ * rate; an element (code * scale) below 2^-126 may count as 0 there, large ones count
+ * whatever their size.  A's codes are a_format, B's are e4m3.
  *
  * The three products of a linear layer y = x W^T with W [n, k], x [t, k]:
  *   y  = zr_matmul_fp8(x, W)                      m, n, k = t, n, k
@@ -119,7 +123,8 @@ ZR_API zr_status zr_matmul_fp8(const uint8_t *a, int64_t lda, const uint8_t *a_s
  *   h    = T(x + residual)     (h = x when residual is NULL)
  *   rstd = 1 / sqrt(mean of h^2 over the row + eps)
  *   y    = h * rstd * weight   in fp32
- * The sum of squares is fp32 in a fixed order.  h, which the next layer adds to
+ * The sum of squares is fp32 in a fixed order (a row whose sum passes fp32's range, with
+ * magnitudes from about 1e19 on, has rstd 0).  h, which the next layer adds to
  * and the backward pass reads, is rounded to T before the norm, so that both
  * passes use the same h.  Outputs, each optional (NULL) but y and q not both:
  *   h          the stream (requires residual); may be exactly x or residual with

@@ -55,7 +55,7 @@ __device__ __forceinline__ uint16_t narrow(float x)
 // Eight elements at p as four words; elements `n` and later are 0.  A whole vector is
 // one access, wherever it starts: the hardware takes 16 bytes at any address, and rows of
 // an odd length need no path of their own (2961 x 402 normed in 6 us, with single
-// elements where rows do not start on 16 bytes 18; 16384 x 4095 in 171, 477; 2413 x 1915
+// elements where rows do not start on 16 bytes 18; 16384 x 4095 in 167, 477; 2413 x 1915
 // quantized both ways in 18, 26).  kStream, here and below: the access carries the
 // non-temporal hint (the builtins themselves: load_stream and store_stream would take the
 // vectors' full alignment for granted).

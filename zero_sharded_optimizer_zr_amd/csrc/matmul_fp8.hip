@@ -298,9 +298,10 @@ __device__ __forceinline__ i32x8 operand(u32x4 lo, u32x4 hi)
 // use.  `split` waves of a workgroup share a tile and take a part of the groups each;
 // their sums meet in LDS and are added in wave order.  So a product with few
 // tiles still occupies the chip, without a workspace.  Bound by the bytes of B and by
-// the latency of the few loads a wave makes: 1 x 11008 x 4096 (m x n x k) 13.6 us, 3.3
-// TB/s; 1 x 32000 x 4096 25.5 us, 5.1 TB/s; 64 x 11008 x 4096 22 us; 1 x 512 x 512 3.5 us,
-// a launch.
+// the latency of the few loads a wave makes: 1 x 11008 x 4096 (m x n x k) 13.7 us, 3.3
+// TB/s; 1 x 32000 x 4096 26 us, 5.0 TB/s; 32 x 11008 x 4096 18 us; 1 x 512 x 512 4 us, a
+// launch.  Rows off 16 bytes have no other kernel: 1000 x 4096 x 4096 50 us (24 on them),
+// 4096 x 4096 x 4096 201 (66).
 constexpr int kSplitThreads = 512;
 constexpr int kSplitWaves = kSplitThreads / 64;
 
@@ -514,8 +515,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // next is loaded, and workgroups stay for several tiles, so that a tile's first loads fall
 // under the last products of the one before.
 //
-// 16384 x 11008 x 4096: 632 us, 2.34 PFLOP/s; 16384 cubed 2.6 PFLOP/s; 11008 x 4096 x 8111
-// (e5m2) 316 us.  A group takes 1.55 us, 0.85 of them products at full clock.  Power is one
+// 16384 x 11008 x 4096: 617 to 654 us (by the card), 2.26 to 2.4 PFLOP/s, accumulating 757 where
+// 642 without; 16384 cubed 2.6 PFLOP/s; 11008 x 4096 x 8111 (e5m2) 308 to 325 us.  A group takes 1.55 us, 0.85 of them products at full clock.  Power is one
 // bound: with zeros for codes a group takes 1.2 us, with random ones the clock falls to 1.9
 // GHz (the matrix unit alone, fed from registers, reaches 4.95 and 4.0 PFLOP/s).  Issue is the
 // other: without loads, reads of LDS and scales the same loop reaches 3.8.  A tile's end
@@ -849,8 +850,8 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_big_kernel(MatmulArgs p, int
 // occupy the chip, and for fp32 outputs.  A group takes 0.5 us for 0.21 us of products:
 // the one wave of a SIMD issues reads, loads and control one after another (the order in
 // which they are spread between the products makes no difference).
-// 1000 x 4096 x 4096 27 us; fp32 outputs, bound by the matrix unit's bf16 rate and by the
-// widening: 11008 x 4096 x 8192 715 us, 1.03 PFLOP/s.
+// 1000 x 4096 x 4096 24 us; fp32 outputs, bound by the matrix unit's bf16 rate and by the
+// widening: 11008 x 4096 x 8192 739 to 757 us (by the card), 1.0 PFLOP/s; accumulating 825.
 constexpr int kMid = 128;
 constexpr int kRing = 4;
 constexpr int kMidOperand = kMid * kGroup;
@@ -1106,9 +1107,9 @@ __global__ __launch_bounds__(kBlock, 1) void matmul_mid_kernel(MatmulArgs p, int
 // multiplies while the other issues its loads.  Each team has a ring of three groups of
 // both operands in LDS; at the end the teams' sums meet there, each team stores half.
 // Against four waves alone: a single wave to a SIMD issues its ~110 instructions of a
-// group one after another, 0.41 us for 0.11 us of products (333 x 4096 x 11008: 41.6 us,
-// 128 x 128 outputs 52); the teams take 38 us, now bound by the loads (24 us with the same
-// loop that loads nothing; 32 us with operands in the last-level cache).  Bringing lines
+// group one after another, 0.41 us for 0.11 us of products (333 x 4096 x 11008 with 128 x
+// 128 outputs: 54 us); the teams take 40 us, now bound by the loads (24 us with the same
+// loop that loads nothing; 29 us with operands in the last-level cache).  Bringing lines
 // into the L2 ahead of the loads, shared out or not, made it slower (43, 52 us).
 constexpr int kPairRows = 128, kPairCols = 64;
 constexpr int kPairThreads = 512;
@@ -1355,17 +1356,21 @@ zr_status split_run(const MatmulArgs &p, hipStream_t st)
 
 // Which kernel.  Times in us on MI355X, operands rotated through more than the caches:
 //  - A split wave's tile is the smallest that leaves at most one workgroup to a compute
-//    unit.  1 x 4096 x 4096: 16 x 16 outputs 6.8, 16 x 32 8.4, 32 x 32 9.3; 1 x 11008 x 4096
-//    (m x n x k): 14.5, 14.3 and, with 16 x 64, 13.6; 32 x 11008 x 4096: 32 x 32 22, 32 x 64
-//    17.5; 64 x 4096 x 4096: 32 x 32 12.2, 64 x 64 20.6; 128 x 4096 x 4096: 32 x 64 16.8, two teams 18.2.
-//  - More tiles than that go to the LDS kernels (250 x 4096 x 11008: 64 x 64 a wave 45, 128 x 64
-//    and two teams 39), up to 16 rows excepted, which are bound by B's bytes either way
-//    (1 x 32000 x 4096: 16 x 32 25.5, 5.1 TB/s).
-//  - One round of 128 x 64 tiles goes to the two teams: 333 x 4096 x 4096 18.5 (128 x 128 by four
-//    waves 24.5), with fp32 outputs 23 (39); 1000 x 1000 x 4000 15.3 (64 x 64 a wave 21.3).  Two
-//    rounds of them lose to one of 128 x 128: 1000 x 4096 x 4096 37.5 and 29 (fp32 53 and 47).
-//  - A round of 256 x 256 tiles costs 9/4 rounds of 128 x 128 (one round each, k = 4096: 50
-//    and 22; 2048 x 4096 x 4096: 54 against 48 for two; 4096 x 4096 x 4096: 64 against 98 for four).
+//    unit.  1 x 4096 x 4096: 16 x 16 outputs 6.6, 16 x 32 8.3, 32 x 32 8.9; 1 x 11008 x 4096
+//    (m x n x k): 16.4, 15.2 and, with 16 x 64, 13.7; 32 x 11008 x 4096: 32 x 32 23, 32 x 64
+//    18; 64 x 4096 x 4096: 32 x 32 12.5, 64 x 64 20.8.  At the upper end of 32 x 64 the two teams
+//    would be faster (128 x 4096 x 4096: 16.5 against 13.5).
+//  - More tiles than that go to the LDS kernels (250 x 4096 x 11008: 64 x 64 a wave 48, 128 x 64
+//    and two teams 42; 17 x 32000 x 4096: 32 x 64 37, 128 x 128 34.5; 64 x 32000 x 4096: 62 and 39),
+//    up to 16 rows excepted, which are bound by B's bytes either way (1 x 32000 x 4096:
+//    16 x 32 26, 16 x 64 35).
+//  - One round of 128 x 64 tiles goes to the two teams: 333 x 4096 x 4096 14.4 (128 x 128 by four
+//    waves 21.3), with fp32 outputs 21 (39); 1000 x 1000 x 4000 14.9 (64 x 64 a wave 21.7).  Two
+//    rounds of them lose to one of 128 x 128: 1000 x 4096 x 4096 29 and 24 (fp32 45 and 41).
+//  - A round of 256 x 256 tiles costs 9/4 rounds of 128 x 128 (one round each, k = 4096: 52
+//    and 24; 2048 x 4096 x 4096: 54 against 47 for two; 4096 x 4096 x 4096: 66 against 97 for four).
+//    A last round of few tiles is where the rule is off by most: 1500 x 11008 x 4096, two
+//    rounds of 256 x 256 for 258 tiles, takes 108 and would take 100 in five of 128 x 128.
 // The LDS kernels load 16 bytes at a time and index a tile's rows in 32 bits; what does
 // not meet that stays with the split waves.
 template <int kFormatA, bool kWide>

@@ -51,8 +51,10 @@ __device__ __forceinline__ u32x2 codes8(u32x4 w, uint32_t s)
 // A row of 16 lanes holds a group, 8 elements per lane, so a wave holds 4
 // consecutive groups (of one row or of consecutive rows) and its accesses cover
 // whole lines; the maximum is four DPP steps.  Each XCD takes 64 consecutive tiles of
-// 16 groups at a time: 8192 x 11008 bf16 in 50 us, 5.4 TB/s (in launch order 56 us).
-// 1 x 4096 takes 2 us, a launch.
+// 16 groups at a time: 8192 x 11008 bf16 in 47 us, 5.7 TB/s (in launch order 56 at a state
+// of 50).  1 x 4096 takes 2 us, a launch.  With rows off 16 bytes the same bytes come from
+// memory, but the vector cache is accessed 2.2 times as often and bounds: 8192 x 4095 in 30
+// us, 8192 x 4096 in 20.
 template <typename T, int kFormat>
 __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(QuantArgs a, int64_t groups)
 {
@@ -94,8 +96,8 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(QuantArgs a, int6
 // LDS, whose 8-byte slots are permuted by the column's lane (slot ^ column / 8) so
 // that the 16 lanes of a write fall into different banks.  Tiles go down the columns
 // (consecutive ones write neighbouring pieces of a transposed row), in runs of 16 to an
-// XCD.  11008 x 4096 in blocks, both copies: 41 us, 4.4 TB/s; 5003 x 12288 by rows and
-// columns: 60 us, 4.1 TB/s: a row of a tile is 256 bytes of a source row and 128 of a
+// XCD.  11008 x 4096 in blocks, both copies: 39 us, 4.6 TB/s (codes alone 30, transpose
+// alone 27); 5003 x 12288 by rows and columns: 57 us, 4.3 TB/s (columns alone 38): a row of a tile is 256 bytes of a source row and 128 of a
 // copy's, shorter runs than a copy's.  The 8 x 8 elements of a thread need the registers
 // of two workgroups to a compute unit: bounded to 4 or 5 they spill (92 and 120 us).
 template <typename T, int kFormat, bool kBlocks>

@@ -96,8 +96,9 @@ __device__ __forceinline__ float block_sum(float v, float (*part)[4], int slot)
     return (part[slot][0] + part[slot][1]) + (part[slot][2] + part[slot][3]);
 }
 
-// Rows of any length: a workgroup per row, read twice (the second time from cache).  h is written in the second read, so that it may replace x
-// or residual.  16384 x 4096 with residual, h, y and codes takes 122 us so.
+// Rows of any length: a workgroup per row, read twice (the second time from cache).  h is
+// written in the second read, so that it may replace x or residual.  4096 x 20000 with
+// residual, h, y and codes: 190 us, 3.9 TB/s.
 template <typename T>
 __global__ __launch_bounds__(kBlock) void norm_wide_kernel(NormArgs a)
 {
@@ -130,8 +131,10 @@ __global__ __launch_bounds__(kBlock) void norm_wide_kernel(NormArgs a)
 
 // Rows held in registers, read once: kWaves waves share a row, a lane holds NV vectors
 // of 8 columns, each wave-wide access covers 512 consecutive columns (four groups).
-// 16384 x 4096 with residual, h, y and codes: 109 us, 5.5 TB/s (without y 84 us); one row
-// of 4096: 3.2 us, a launch and one round trip to memory.
+// 16384 x 4096 with residual, h, y and codes: 105 us, 5.7 TB/s (without y 81 us); one row
+// of 4096: 3.2 us, a launch and one round trip to memory.  With 4095 columns, where rows start
+// at any element, the bytes from and to memory are the same to 3 %, but the vector cache is
+// accessed 2.7 times as often and bounds: 167 us.
 template <typename T, int NV, int kWaves>
 __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : kBlock) void norm_row_kernel(NormArgs a)
 {
@@ -232,8 +235,9 @@ __device__ __forceinline__ float dx_factor(float dot, float rstd, int64_t cols)
     return __fdiv_rn(dot, (float)cols) * rstd * rstd;
 }
 
-// dx for rows of any length, read twice.  With the partial sums of the
-// weight gradient, which read dy and h once more by columns, 16384 x 4096 takes 383 us so.
+// dx for rows of any length, read twice.  With the partial sums of the weight gradient,
+// which read dy and h once more by columns, 4096 x 20000 with dh takes 260 us, 2.5 TB/s of
+// what has to move.
 template <typename T>
 __global__ __launch_bounds__(kBlock) void norm_dx_wide_kernel(NormGradArgs a)
 {
@@ -277,8 +281,10 @@ __global__ __launch_bounds__(kBlock) void norm_dweight_partial_kernel(NormGradAr
 // waves share a row, a workgroup takes kSlots rows at a time, every parts * kSlots'th,
 // and reads the next rows before it reduces the present ones.  A lane sums the weight
 // gradient of its columns over its rows; the slots meet in LDS, in slot order.
-// 16384 x 4096 with dh: 106 us, 5.05 TB/s, the partial sums' own pass included; 777 x 1000:
-// 10 us, two launches.
+// 16384 x 4096 with dh: 104 us, 5.2 TB/s, the partial sums' own pass included; 8192 x 11008
+// 153 us, 4.7 TB/s; 777 x 1000 10 us, two launches.  Fewer rounds to a workgroup overlap less, and
+// the partial sums weigh more: 8192 x 1024 19.5 us, 3.4 TB/s.  Rows off 16 bytes are bound by the
+// vector cache, as in the forward pass: 16384 x 4095 237 us, 4096 x 1257 24.
 constexpr int kGradThreads = 512;
 
 template <typename T, int NV, int kWaves>
