@@ -515,9 +515,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // next is loaded, and workgroups stay for several tiles, so that a tile's first loads fall
 // under the last products of the one before.
 //
-// 16384 x 11008 x 4096: 617 to 654 us (by the card), 2.26 to 2.4 PFLOP/s, accumulating 757 where
-// 642 without; 16384 cubed 2.6 PFLOP/s; 11008 x 4096 x 8111 (e5m2) 308 to 325 us.  A group takes 1.55 us, 0.85 of them products at full clock.  Power is one
-// bound: with zeros for codes a group takes 1.2 us, with random ones the clock falls to 1.9
+// 16384 x 11008 x 4096: 617 to 654 us (by the card), 2.26 to 2.4 PFLOP/s, accumulating 757
+// where 642 without; 16384 cubed 2.6 PFLOP/s; 11008 x 4096 x 8111 (e5m2) 306 to 325 us.  A
+// group takes 1.55 us, 0.85 of them products at full clock.  Power is one bound: with zeros for codes a group takes 1.2 us, with random ones the clock falls to 1.9
 // GHz (the matrix unit alone, fed from registers, reaches 4.95 and 4.0 PFLOP/s).  Issue is the
 // other: without loads, reads of LDS and scales the same loop reaches 3.8.  A tile's end
 // takes 9.5 us, in which all workgroups store 33 MB at once.  Measured and not kept: 16 x 16 x

@@ -97,8 +97,8 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(QuantArgs a, int6
 // that the 16 lanes of a write fall into different banks.  Tiles go down the columns
 // (consecutive ones write neighbouring pieces of a transposed row), in runs of 16 to an
 // XCD.  11008 x 4096 in blocks, both copies: 39 us, 4.6 TB/s (codes alone 30, transpose
-// alone 27); 5003 x 12288 by rows and columns: 57 us, 4.3 TB/s (columns alone 38): a row of a tile is 256 bytes of a source row and 128 of a
-// copy's, shorter runs than a copy's.  The 8 x 8 elements of a thread need the registers
+// alone 27); 5003 x 12288 by rows and columns: 57 us, 4.3 TB/s (columns alone 38): a row of
+// a tile is 256 bytes of a source row and 128 of a copy's, shorter runs than a copy's.  The 8 x 8 elements of a thread need the registers
 // of two workgroups to a compute unit: bounded to 4 or 5 they spill (92 and 120 us).
 template <typename T, int kFormat, bool kBlocks>
 __global__ __launch_bounds__(kBlock) void quantize_tile_kernel(QuantArgs a, int64_t tiles)
