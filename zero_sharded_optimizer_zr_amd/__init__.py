@@ -3,7 +3,8 @@ an AMD Instinct MI355X.
 
 Argument marshalling only.  Every function has the name of the C entry point
 it calls (declared in ``include/zr.h``, the 8-bit floating-point operators in
-``include/zr_fp8.h``); every step of the path runs in the
+``include/zr_fp8.h``, clipping in ``include/zr_clip.h``, the head norms with
+rotation in ``include/zr_rope.h``); every step of the path runs in the
 library's HIP kernels.  PyTorch provides device memory (``torch.Tensor``) and
 streams.  Importing fails loudly if ``libzr.so`` has not been built.
 
@@ -31,6 +32,10 @@ __all__ = [
     "zr_graph_destroy", "zr_last_error", "zr_abi_version", "LIBRARY", "SYMBOLS",
     "zr_quantize_fp8", "zr_matmul_fp8", "zr_rmsnorm_fp8", "zr_rmsnorm_backward", "fp8_matrix", "rmsnorm_workspace",
     "FP8_SYMBOLS", "ZR_FP8_GROUP", "ZR_RMSNORM_PARTIALS",
+    "zr_grad_norm", "zr_clip_grads", "zr_adamw_step_clip", "zr_adamw_step_clip_f16", "TensorList", "tensor_list",
+    "clip_record", "grad_norm_workspace", "CLIP_SYMBOLS", "ZR_GRAD_NORM_PARTIALS",
+    "zr_qk_norm_rope", "zr_qk_norm_rope_backward", "Rope", "rope", "qk_norm_workspace", "ROPE_SYMBOLS",
+    "ZR_MAX_HEAD_DIM", "ZR_MAX_ROPE_AXES", "ZR_QK_PARTIALS",
 ]
 
 LIBRARY = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libzr.so")
@@ -70,6 +75,20 @@ class _HParams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
                 ("step", ctypes.c_int64)]
+
+
+class _ClipHParams(ctypes.Structure):
+    _fields_ = [("max_norm", ctypes.c_double), ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("heads", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
@@ -116,13 +135,26 @@ _FP8_SIGS = {
                         _P, _P], _I32),
     "zr_rmsnorm_backward": ([_P, _I64, _P, _I64, _P, _P, _P, _I64, _I32, _I64, _I64, _P, _I64, _P, _P, _P], _I32),
 }
-for _name, (_args, _res) in (_SIGS | _FP8_SIGS).items():
+_CLIP_SIGS = {
+    "zr_grad_norm": ([_P, _P, _I32, _I32, _P, _I32, _P, _P, _P, _P], _I32),
+    "zr_clip_grads": ([_P, _P, _I32, _I32, _P, _P], _I32),
+    "zr_adamw_step_clip": ([_P, _P, _P, _P, _P, _I64, _P, _P, _P], _I32),
+    "zr_adamw_step_clip_f16": ([_P, _P, _P, _P, _P, _I64, _P, _P, _P, _P], _I32),
+}
+_ROPE_SIGS = {
+    "zr_qk_norm_rope": ([_P, _P, _P, _P, _I32, _I64, _I64, ctypes.c_double, _P, _I64, _P, _P, _P, _P], _I32),
+    "zr_qk_norm_rope_backward": ([_P, _P, _P, _P, _P, _P, _I32, _I64, _I64, ctypes.c_double, _P, _I64, _P, _P, _P, _P,
+                                  _P, _P, _P], _I32),
+}
+for _name, (_args, _res) in (_SIGS | _FP8_SIGS | _CLIP_SIGS | _ROPE_SIGS).items():
     _f = getattr(_lib, _name)
     _f.argtypes = _args
     _f.restype = _res
 
 SYMBOLS = tuple(_SIGS)          # zr.h
 FP8_SYMBOLS = tuple(_FP8_SIGS)  # zr_fp8.h
+CLIP_SYMBOLS = tuple(_CLIP_SIGS)  # zr_clip.h
+ROPE_SYMBOLS = tuple(_ROPE_SIGS)  # zr_rope.h
 
 
 def zr_last_error() -> str:
@@ -811,3 +843,251 @@ def zr_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     p_ws = _vector(workspace, (torch.float32,), ZR_RMSNORM_PARTIALS * cols, "workspace")
     _gpu_call_flat(_lib.zr_rmsnorm_backward, stream, (dy, h, weight, rstd, dx, dweight, workspace, dh), p_dy, lddy,
                    p_h, ldh, p_w, p_rstd, p_dh, lddh, _DTYPES[h.dtype], rows, cols, p_dx, lddx, p_dw, p_ws)
+
+
+# ----------------------------------------------- clipping by the gradient norm ----
+
+ZR_GRAD_NORM_PARTIALS = 2048
+
+
+class TensorList:
+    """Tensors of one dtype and device, as zr_grad_norm and zr_clip_grads take them: made
+    once (tensor_list) and kept, it spares those calls the checks of every tensor.  It
+    holds the tensors; their memory must stay where it is (no resize_ or set_)."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor]):
+        self.tensors = tuple(tensors)
+        self.device = self.dtype = None
+        for i, t in enumerate(self.tensors):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"tensors[{i}] must be a torch.Tensor")
+            _typed(t, _DTYPES, f"tensors[{i}]")
+            if not t.is_contiguous():
+                raise ValueError(f"tensors[{i}] must be contiguous")
+            if i and t.dtype != self.dtype:
+                raise TypeError(f"tensors[{i}] is {t.dtype}, the tensors before it {self.dtype}")
+            if i and t.device != self.device:
+                raise ValueError(f"tensors[{i}] is on {t.device}, the tensors before it on {self.device}")
+            self.dtype, self.device = t.dtype, t.device
+        n = len(self.tensors)
+        self.ptrs = (ctypes.c_void_p * max(1, n))(*[t.data_ptr() or None for t in self.tensors])
+        self.numels = (ctypes.c_int64 * max(1, n))(*[t.numel() for t in self.tensors])
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def tensor_list(tensors: Sequence[torch.Tensor]) -> TensorList:
+    """The tensors (bf16, fp16 or fp32, one dtype, one device, contiguous) as a list that a
+    program keeps from step to step."""
+    return TensorList(tensors)
+
+
+def clip_record(device=None) -> torch.Tensor:
+    """A device tensor holding one zr_clip record (16 bytes), uninitialised: [0] is the sum of
+    squares in fp64 (what the ranks all-reduce), .view(torch.float32)[2] the norm and [3] the
+    factor."""
+    return torch.empty(2, dtype=torch.float64, device=device if device is not None else "cuda")
+
+
+def grad_norm_workspace(device=None) -> torch.Tensor:
+    """Workspace of zr_grad_norm."""
+    return torch.empty(ZR_GRAD_NORM_PARTIALS, dtype=torch.float64, device=device if device is not None else "cuda")
+
+
+def _clip(clip: torch.Tensor) -> Optional[int]:
+    return _vector(clip, (torch.float64,), 2, "clip")
+
+
+def _list(grads) -> TensorList:
+    return grads if isinstance(grads, TensorList) else TensorList(grads)
+
+
+def zr_grad_norm(grads: Union[TensorList, Sequence[torch.Tensor]], clip: torch.Tensor, workspace: torch.Tensor, *,
+                 max_norm: float = float("inf"), eps: float = 1e-6, grad_scale: float = 1.0, accumulate: bool = False,
+                 ls: Optional[torch.Tensor] = None, stream=None) -> None:
+    """clip <- the sum of squares of all elements of grads (added to what it holds with
+    accumulate), norm = |grad_scale| * sqrt(sum) / ls's scale and factor = min(1, max_norm /
+    (norm + eps)).  ls (fp16 gradients) gets its overflow flag set if the sum is not finite.
+    Ranks that each hold a part all-reduce clip[:1] and call again with accumulate and the
+    tensors that all hold, or none."""
+    grads = _list(grads)
+    hp = _ClipHParams(float(max_norm), float(eps), float(grad_scale))
+    p_ws = _vector(workspace, (torch.float64,), ZR_GRAD_NORM_PARTIALS, "workspace")
+    _gpu_call_flat(_lib.zr_grad_norm, stream, (*grads.tensors[:1], clip, workspace, ls), grads.ptrs, grads.numels,
+                   len(grads), _DTYPES[grads.dtype or torch.float32], ctypes.byref(hp), int(bool(accumulate)), _ls(ls),
+                   _clip(clip), p_ws)
+
+
+def zr_clip_grads(grads: Union[TensorList, Sequence[torch.Tensor]], clip: torch.Tensor, stream=None) -> None:
+    """Every element of grads times the factor in clip, in place."""
+    grads = _list(grads)
+    _gpu_call_flat(_lib.zr_clip_grads, stream, (*grads.tensors[:1], clip), grads.ptrs, grads.numels, len(grads),
+                   _DTYPES[grads.dtype or torch.float32], _clip(clip))
+
+
+def zr_adamw_step_clip(grad: torch.Tensor, master: torch.Tensor, exp_avg: torch.Tensor, exp_avg_sq: torch.Tensor,
+                       param_out: Optional[torch.Tensor], clip: torch.Tensor, *, lr: float, beta1: float, beta2: float,
+                       eps: float, weight_decay: float, step: int, grad_scale: float = 1.0,
+                       numel: Optional[int] = None, stream=None) -> None:
+    """zr_adamw_step on the gradient times the factor in clip."""
+    hp = _HParams(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), float(grad_scale),
+                  int(step))
+    numel = master.numel() if numel is None else int(numel)
+    _need(numel, grad=grad, master=master, exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, param_out=param_out)
+    _gpu_call(_lib.zr_adamw_step_clip, stream, (grad, master, exp_avg, exp_avg_sq, param_out, clip),
+              _ptr(grad, 2, "grad"), _ptr(master, 4, "master"), _ptr(exp_avg, 4, "exp_avg"),
+              _ptr(exp_avg_sq, 4, "exp_avg_sq"), _ptr(param_out, 2, "param_out"), numel, ctypes.byref(hp), _clip(clip))
+
+
+def zr_adamw_step_clip_f16(grad: torch.Tensor, master: torch.Tensor, exp_avg: torch.Tensor, exp_avg_sq: torch.Tensor,
+                           param_out: Optional[torch.Tensor], ls: torch.Tensor, clip: torch.Tensor, *, lr: float,
+                           beta1: float, beta2: float, eps: float, weight_decay: float, step: int,
+                           grad_scale: float = 1.0, numel: Optional[int] = None, stream=None) -> None:
+    """zr_adamw_step_f16 on the unscaled gradient times the factor in clip."""
+    hp = _HParams(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), float(grad_scale),
+                  int(step))
+    numel = master.numel() if numel is None else int(numel)
+    _need(numel, grad=grad, master=master, exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, param_out=param_out)
+    _gpu_call(_lib.zr_adamw_step_clip_f16, stream, (grad, master, exp_avg, exp_avg_sq, param_out, ls, clip),
+              _ptr(grad, 2, "grad"), _ptr(master, 4, "master"), _ptr(exp_avg, 4, "exp_avg"),
+              _ptr(exp_avg_sq, 4, "exp_avg_sq"), _ptr(param_out, 2, "param_out"), numel, ctypes.byref(hp), _ls(ls),
+              _clip(clip))
+
+
+# --------------------------------------------------- head norms with rotation ----
+
+ZR_MAX_HEAD_DIM = 512
+ZR_MAX_ROPE_AXES = 4
+ZR_QK_PARTIALS = 512
+
+
+class Rope:
+    """How zr_qk_norm_rope turns pairs; a program makes it once (rope)."""
+
+    def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False, pair_axis: Optional[Sequence[int]] = None):
+        p = _vector(inv_freq, (torch.float32,), 0, "inv_freq")
+        half = inv_freq.numel()
+        if 2 * half > ZR_MAX_HEAD_DIM:
+            raise ValueError(f"inv_freq holds {half} frequencies, at most {ZR_MAX_HEAD_DIM // 2} fit a head")
+        axis = None if pair_axis is None else bytes(int(x) for x in pair_axis)
+        if axis is not None and len(axis) != half:
+            raise ValueError(f"pair_axis holds {len(axis)} entries, inv_freq {half}")
+        if axis and max(axis) >= ZR_MAX_ROPE_AXES:
+            raise ValueError(f"pair_axis names axis {max(axis)}, at most {ZR_MAX_ROPE_AXES} axes are there")
+        self.inv_freq, self.axes = inv_freq, 1 + max(axis) if axis else 1
+        self._axis = (ctypes.c_uint8 * max(1, half))(*axis) if axis is not None else None
+        self.c = _Rope(p, None if axis is None else ctypes.addressof(self._axis), 2 * half, self.axes,
+                       int(bool(interleaved)))
+
+
+def rope(inv_freq: torch.Tensor, *, interleaved: bool = False, pair_axis: Optional[Sequence[int]] = None) -> Rope:
+    """Rotation of the first 2 * len(inv_freq) elements of a head: pair j by position *
+    inv_freq[j] (fp32, on the GPU), pairs half the turned part apart or, interleaved,
+    neighbours.  pair_axis[j] is the axis (0 time, 1 height, ...) whose position turns pair j."""
+    return Rope(inv_freq, interleaved, pair_axis)
+
+
+def qk_norm_workspace(head_dim: int, device=None) -> torch.Tensor:
+    """Workspace of zr_qk_norm_rope_backward."""
+    return torch.empty(ZR_QK_PARTIALS, head_dim, dtype=torch.float32, device=device if device is not None else "cuda")
+
+
+def _heads(t: Optional[torch.Tensor], dtype, name: str, shape=None):
+    """A tensor [tokens, heads, head_dim] with contiguous rows as a zr_heads (None for None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    own = t.shape
+    if len(own) != 3:
+        raise ValueError(f"{name} must have three dimensions: tokens, heads, head_dim")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and own != shape:
+        raise ValueError(f"{name} is {tuple(own)}, {tuple(shape)} needed")
+    strides = t.stride()
+    if own[2] > 1 and strides[2] != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return _Heads(t.data_ptr() or None, own[1], strides[0], strides[1])
+
+
+def _positions(positions: Optional[torch.Tensor], tokens: int, axes: int):
+    """(address, distance between axes) of positions [tokens] or [axes, tokens]."""
+    if positions is None:
+        return None, 0
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    if positions.dtype != torch.int64:
+        raise TypeError(f"positions must be torch.int64, not {positions.dtype}")
+    shape, strides = positions.shape, positions.stride()
+    if (shape != (tokens,) or axes > 1) and (len(shape) != 2 or shape[0] < axes or shape[1] != tokens):
+        raise ValueError(f"positions is {tuple(shape)}, {(axes, tokens) if axes > 1 else (tokens,)} needed")
+    if tokens > 1 and strides[-1] != 1:
+        raise ValueError("positions must be contiguous along the tokens")
+    return positions.data_ptr() or None, strides[0] if len(shape) == 2 else tokens
+
+
+def _ref(c):
+    return None if c is None else ctypes.byref(c)
+
+
+def _qk(q, k):
+    """(dtype, tokens, head_dim) of queries and keys; either may be None."""
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("neither q nor k given")
+    if not isinstance(one, torch.Tensor):
+        raise TypeError("q and k must be torch.Tensors")
+    _typed(one, (torch.bfloat16, torch.float16), "q and k")
+    if len(one.shape) != 3:
+        raise ValueError("q and k must have three dimensions: tokens, heads, head_dim")
+    if q is not None and k is not None and (len(k.shape) != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]):
+        raise ValueError(f"q is {tuple(q.shape)} and k {tuple(k.shape)}: tokens and head_dim must agree")
+    return one.dtype, one.shape[0], one.shape[2]
+
+
+def zr_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+                    k_weight: Optional[torch.Tensor], positions: Optional[torch.Tensor], rope: Rope,
+                    q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor], *, eps: float = 1e-5,
+                    stream=None) -> None:
+    """q_out, k_out [tokens, heads, head_dim] = the heads of q, k divided by their root mean
+    square, times q_weight, k_weight [head_dim] (None: not normed), and turned by their
+    positions (int64 [tokens], or [axes, tokens] for rope's axes).  q or k may be None; q_out
+    may be q, k_out k.  Tokens and heads may have any strides (slices of the fused
+    product's rows)."""
+    kind, tokens, dim = _qk(q, k)
+    c_q, c_k = _heads(q, kind, "q"), _heads(k, kind, "k")
+    c_qo = _heads(q_out, kind, "q_out", q.shape if q is not None else None)
+    c_ko = _heads(k_out, kind, "k_out", k.shape if k is not None else None)
+    p_pos, stride = _positions(positions, tokens, rope.axes)
+    p_qw, p_kw = _vector(q_weight, (kind,), dim, "q_weight"), _vector(k_weight, (kind,), dim, "k_weight")
+    _gpu_call_flat(_lib.zr_qk_norm_rope, stream, (q, k, q_weight, k_weight, positions, rope.inv_freq, q_out, k_out),
+                   _ref(c_q), _ref(c_k), p_qw, p_kw, _DTYPES[kind], tokens, dim, float(eps), p_pos, stride,
+                   ctypes.byref(rope.c), _ref(c_qo), _ref(c_ko))
+
+
+def zr_qk_norm_rope_backward(dq: Optional[torch.Tensor], dk: Optional[torch.Tensor], q: Optional[torch.Tensor],
+                             k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+                             k_weight: Optional[torch.Tensor], positions: Optional[torch.Tensor], rope: Rope,
+                             dq_in: Optional[torch.Tensor], dk_in: Optional[torch.Tensor],
+                             dq_weight: Optional[torch.Tensor] = None, dk_weight: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None, *, eps: float = 1e-5, stream=None) -> None:
+    """Gradients of zr_qk_norm_rope: dq_in, dk_in of its inputs and dq_weight, dk_weight, from
+    dq, dk of its outputs, through a workspace of qk_norm_workspace(head_dim).  q and k are the
+    forward pass's inputs (not read, and may be None, without a weight).  dq_in may be dq or
+    q, dk_in dk or k."""
+    kind, tokens, dim = _qk(dq, dk)
+    shape_q, shape_k = dq.shape if dq is not None else None, dk.shape if dk is not None else None
+    c_dq, c_dk = _heads(dq, kind, "dq"), _heads(dk, kind, "dk")
+    c_q, c_k = _heads(q, kind, "q", shape_q), _heads(k, kind, "k", shape_k)
+    c_qi, c_ki = _heads(dq_in, kind, "dq_in", shape_q), _heads(dk_in, kind, "dk_in", shape_k)
+    p_pos, stride = _positions(positions, tokens, rope.axes)
+    p_qw, p_kw = _vector(q_weight, (kind,), dim, "q_weight"), _vector(k_weight, (kind,), dim, "k_weight")
+    p_dqw, p_dkw = _vector(dq_weight, (kind,), dim, "dq_weight"), _vector(dk_weight, (kind,), dim, "dk_weight")
+    p_ws = _vector(workspace, (torch.float32,), ZR_QK_PARTIALS * dim, "workspace")
+    _gpu_call_flat(_lib.zr_qk_norm_rope_backward, stream,
+                   (dq, dk, q, k, q_weight, k_weight, positions, rope.inv_freq, dq_in, dk_in, dq_weight, dk_weight,
+                    workspace),
+                   _ref(c_dq), _ref(c_dk), _ref(c_q), _ref(c_k), p_qw, p_kw, _DTYPES[kind], tokens, dim, float(eps),
+                   p_pos, stride, ctypes.byref(rope.c), _ref(c_qi), _ref(c_ki), p_dqw, p_dkw, p_ws)

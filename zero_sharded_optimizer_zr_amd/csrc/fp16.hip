@@ -21,27 +21,9 @@
 // a full grid, non-temporal 16-byte accesses, residency capped with reserved
 // LDS), with fp16 <-> fp32 done by the hardware conversions (exact widening;
 // round to nearest even for the narrowing, NaN canonicalised to sign | 0x7e00).
-#include "zr_math.hpp"
+#include "fp16.hpp"
 
 namespace zr {
-
-// ----------------------------------------------------------- fp16 helpers ----
-
-__device__ __forceinline__ float f16_to_f32(uint32_t h16)
-{
-    return (float)__builtin_bit_cast(_Float16, (uint16_t)h16);
-}
-__device__ __forceinline__ float f16_lo(uint32_t w) { return f16_to_f32(w & 0xffffu); }
-__device__ __forceinline__ float f16_hi(uint32_t w) { return f16_to_f32(w >> 16); }
-
-// fp32 -> fp16 bits, round to nearest even (hardware), NaN -> sign | 0x7e00.
-__device__ __forceinline__ uint32_t f32_to_f16(float f)
-{
-    uint32_t h = __builtin_bit_cast(uint16_t, (_Float16)f);
-    return (f != f) ? (((__float_as_uint(f) >> 16) & 0x8000u) | 0x7e00u) : h;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) { return f32_to_f16(lo) | (f32_to_f16(hi) << 16); }
 
 __device__ __forceinline__ bool f16_nonfinite(uint32_t h16) { return (h16 & 0x7c00u) == 0x7c00u; }
 
@@ -356,15 +338,6 @@ static zr_status reduce_f16_launch(const void *const *contribs, int32_t n, int64
     const size_t lds = n > 8 ? 80 * 1024 : (n > 4 ? 40 * 1024 : 32 * 1024);
     return launch(reduce_f16_vec_kernel<MaxN>, order_grid<MaxN <= 8 ? kReduceOrder : kReduceWideOrder>(tiles),
                   dim3(kBlock), lds, st, c, n, out, numel, head, groups, d, ls);
-}
-
-inline zr_status check_ls(const char *who, const void *ls)
-{
-    if (!ls)
-        return fail(ZR_EINVAL, "%s: loss-scale record is NULL", who);
-    if (!aligned_to(ls, 4))
-        return fail(ZR_EALIGN, "%s: loss-scale record must be 4-byte aligned", who);
-    return ZR_OK;
 }
 
 int fp16_scalar_slots(ScalarSlot *out)

@@ -28,14 +28,18 @@ struct zr_graph {
 };
 
 namespace zr {
+
+int clip_scalar_slots(ScalarSlot *out);  // clip.hip
+
 namespace {
 
 std::vector<ScalarSlot> all_slots()
 {
-    std::vector<ScalarSlot> v(3 * kMaxScalarSlots);
+    std::vector<ScalarSlot> v(4 * kMaxScalarSlots);
     int k = adamw_scalar_slots(v.data());
     k += fused_scalar_slots(v.data() + k);
     k += fp16_scalar_slots(v.data() + k);
+    k += clip_scalar_slots(v.data() + k);
     v.resize(k);
     return v;
 }
