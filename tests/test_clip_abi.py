@@ -65,7 +65,7 @@ WORK = 8 * zr.ZR_GRAD_NORM_PARTIALS
     (dict(eps=nan), 1), (dict(grad_scale=inf), 1), (dict(grad_scale=nan), 1), (dict(accumulate=2), 1),
     (dict(clip=None), 1), (dict(workspace=None), 1), (dict(clip=at(4, 4)), 3), (dict(workspace=at(5, 4)), 3),
     (dict(ls=at(3, 2)), 3), (dict(items=((at(0), -1),)), 1), (dict(items=((None, 1),)), 1),
-    (dict(items=((at(0), (1 << 44) + 1),)), 1), (dict(items=((at(0, 1), 8),)), 3),
+    (dict(items=((at(0), (1 << 42) + 1),)), 1), (dict(items=((at(0, 1), 8),)), 3),
     (dict(items=((at(0, 2), 8),), dtype=2), 3), (dict(clip=at(5, WORK - 8)), 1), (dict(ls=at(4, 12)), 1),
     (dict(ls=at(5, WORK - 4)), 1), (dict(items=((at(4, -18), 10),)), 1), (dict(items=((at(5, WORK - 2), 10),)), 1),
     (dict(items=((at(0), 5), (at(3, -2), 2),)), 1)])

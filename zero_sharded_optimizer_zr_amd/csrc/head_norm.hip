@@ -33,8 +33,10 @@ struct RopeArgs {
     const int64_t *positions;
     const float *inv_freq;
     float *partial;
-    int32_t dim, rot, interleaved, parts[2];
-    float eps;
+    int32_t dim, rot, axes, interleaved;
+    int32_t parts[2];  // units of a token (forward) or sums (backward) of each tensor
+    int32_t per[2];    // steps of a unit
+    float eps, inv_dim;
     uint8_t axis[kMaxPairs];
 };
 
@@ -47,11 +49,17 @@ struct Vec<8> {
 };
 template <>
 struct Vec<4> {
-    typedef any_u32x2 type;
+    typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2)));
+};
+template <>
+struct Vec<2> {
+    typedef uint32_t type __attribute__((ext_vector_type(1), aligned(2)));
 };
 
-// Where a lane's chunk lies in a row: the first elements of its two vectors.  `second` is
-// false where the second (single-element chunks of an odd rest) is past the row.
+// Where a lane's chunk lies in a row: V elements of the first and V of the second half of
+// the turned part (or, behind it, of the rest), so that neighbouring lanes load
+// neighbouring vectors.  Single-element chunks of an odd rest: `second` is false where the
+// row has no second element.  Places outside the row are moved to one inside.
 struct Chunk {
     int32_t first, other;
     bool live, second, turned;
@@ -60,61 +68,142 @@ struct Chunk {
 template <int V>
 __device__ __forceinline__ Chunk chunk_of(int32_t c, const RopeArgs &a)
 {
-    const int32_t turned = a.rot / (2 * V);
+    const int32_t turned = a.rot / (2 * V), rest = a.dim - a.rot;
     Chunk k;
     k.turned = c < turned;
-    const bool halves = k.turned && !a.interleaved;
-    k.first = halves ? V * c : 2 * V * c;
-    k.other = halves ? a.rot / 2 + V * c : 2 * V * c + V;
-    k.live = k.first < a.dim;
-    k.second = k.other < a.dim;
+    if (V == 1 && a.interleaved && k.turned) {
+        k.first = 2 * c;
+        k.other = 2 * c + 1;
+    } else if (k.turned) {
+        k.first = V * c;
+        k.other = a.rot / 2 + V * c;
+    } else {
+        k.first = a.rot + V * (c - turned);
+        k.other = k.first + (rest + 1) / 2;
+    }
+    k.live = c < turned + (rest + 2 * V - 1) / (2 * V);
+    k.second = k.live && k.other < a.dim;
+    if (!k.live)
+        k.first = 0;
+    if (!k.second)
+        k.other = k.first;
     return k;
 }
 
-// A chunk as pairs, one to a word.
-template <int V>
-__device__ __forceinline__ void load_pairs(const uint16_t *row, const Chunk &k, bool live, int32_t interleaved,
-                                           uint32_t (&w)[V])
-{
-    if constexpr (V == 1) {
-        w[0] = 0;
-        if (live) {
-            w[0] = load_global(row + k.first);
-            if (k.second)
-                w[0] |= (uint32_t)load_global(row + k.other) << 16;
-        }
-    } else {
-        typedef typename Vec<V>::type vec;
-        vec p{}, q{};
-        if (live) {
-            p = *(global_ptr<const vec>)(row + k.first);
-            q = *(global_ptr<const vec>)(row + k.other);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t halves = __builtin_amdgcn_perm(q[i / 2], p[i / 2], i % 2 ? 0x07060302 : 0x05040100);
-            w[i] = interleaved ? (i < V / 2 ? p[i % (V / 2)] : q[i % (V / 2)]) : halves;
-        }
+// A chunk's words, a pair to a word, are made of its two vectors' words p, q by byte
+// permutes: words 2i and 2i + 1 are the low and the high halves of q[i] and p[i] where pairs
+// are halves of the row apart, and p[i] and q[i] themselves where they are neighbours.  The
+// same selectors turn the words back.
+struct Selectors {
+    uint32_t even, odd;
+
+    __device__ __forceinline__ explicit Selectors(const RopeArgs &a)
+        : even(a.interleaved ? 0x03020100u : 0x05040100u), odd(a.interleaved ? 0x07060504u : 0x07060302u)
+    {
     }
+};
+
+// The pair in word e of chunk c.
+template <int V>
+__device__ __forceinline__ int32_t pair_of(int32_t c, int e, const RopeArgs &a)
+{
+    if (V > 1 && a.interleaved)
+        return (e % 2 ? a.rot / 4 : 0) + V / 2 * c + e / 2;
+    return V * c + e;
 }
 
+// The column of element b (0: first, 1: second) of word e.
 template <int V>
-__device__ __forceinline__ void store_pairs(uint16_t *row, const Chunk &k, int32_t interleaved, const uint32_t (&w)[V])
+__device__ __forceinline__ int32_t column_of(const Chunk &k, int e, int b, const RopeArgs &a)
+{
+    if (V > 1 && a.interleaved)
+        return (e % 2 ? k.other : k.first) + e / 2 * 2 + b;
+    return (b ? k.other : k.first) + e;
+}
+
+// A lane's place in the rows of one buffer: the offsets of its chunks' two vectors from the
+// first head of a step.
+template <int V, int kChunks>
+struct Offsets {
+    int64_t head, first[kChunks], other[kChunks];
+
+    __device__ __forceinline__ Offsets(const Chunk (&k)[kChunks], int32_t group, int64_t head_stride)
+        : head(group * head_stride)
+    {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            first[i] = head + k[i].first;
+            other[i] = head + k[i].other;
+        }
+    }
+};
+
+// A row's chunks as they lie in memory.  Every lane loads: one whose chunk is not in the
+// row (or whose head is not there) loads another's, which is not used, so that no load waits
+// for a branch and none is used before all of them are on their way.
+template <int V, int kChunks>
+struct Loaded {
+    typename Vec<V>::type p[kChunks], q[kChunks];
+
+    // `step` points to the step's first head; where the lane's own head is not there (`back`)
+    // it takes that one.
+    __device__ __forceinline__ void load(const uint16_t *step, const Offsets<V, kChunks> &o, bool back)
+    {
+        typedef typename Vec<V>::type vec;
+        const uint16_t *row = step - (back ? o.head : 0);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            p[i] = *(global_ptr<const vec>)(row + o.first[i]);
+            q[i] = *(global_ptr<const vec>)(row + o.other[i]);
+        }
+    }
+
+    __device__ __forceinline__ void pairs(int i, const Chunk &, const Selectors &sel, uint32_t (&w)[V]) const
+    {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            w[e] = __builtin_amdgcn_perm(q[i][e / 2], p[i][e / 2], e % 2 ? sel.odd : sel.even);
+    }
+};
+
+template <int kChunks>
+struct Loaded<1, kChunks> {
+    uint16_t p[kChunks], q[kChunks];
+
+    __device__ __forceinline__ void load(const uint16_t *step, const Offsets<1, kChunks> &o, bool back)
+    {
+        const uint16_t *row = step - (back ? o.head : 0);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            p[i] = load_global(row + o.first[i]);
+            q[i] = load_global(row + o.other[i]);
+        }
+    }
+
+    __device__ __forceinline__ void pairs(int i, const Chunk &k, const Selectors &, uint32_t (&w)[1]) const
+    {
+        w[0] = p[i] | (k.second ? (uint32_t)q[i] << 16 : 0);
+    }
+};
+
+template <int V, int kChunks>
+__device__ __forceinline__ void store_pairs(uint16_t *step, const Offsets<V, kChunks> &o, int i, const Chunk &k,
+                                            const Selectors &sel, const uint32_t (&w)[V])
 {
     if constexpr (V == 1) {
-        *(global_ptr<uint16_t>)(row + k.first) = (uint16_t)w[0];
+        *(global_ptr<uint16_t>)(step + o.first[i]) = (uint16_t)w[0];
         if (k.second)
-            *(global_ptr<uint16_t>)(row + k.other) = (uint16_t)(w[0] >> 16);
+            *(global_ptr<uint16_t>)(step + o.other[i]) = (uint16_t)(w[0] >> 16);
     } else {
         typedef typename Vec<V>::type vec;
         vec p, q;
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            p[i] = interleaved ? w[i] : __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x05040100);
-            q[i] = interleaved ? w[V / 2 + i] : __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x07060302);
+        for (int j = 0; j < V / 2; ++j) {
+            p[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], sel.even);
+            q[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], sel.odd);
         }
-        *(global_ptr<vec>)(row + k.first) = p;
-        *(global_ptr<vec>)(row + k.other) = q;
+        __builtin_nontemporal_store(p, (global_ptr<vec>)(step + o.first[i]));
+        __builtin_nontemporal_store(q, (global_ptr<vec>)(step + o.other[i]));
     }
 }
 
@@ -146,114 +235,253 @@ __device__ __forceinline__ void wave_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
-// Cosines and sines of a token's pairs, a pair to a lane at a time, in the wave's own LDS.
-__device__ __forceinline__ void turn_pairs(const RopeArgs &a, int64_t token, float2 *turn)
-{
-    wave_fence();  // the token before has been read
-    for (int32_t j = threadIdx.x & 63; j < a.rot / 2; j += 64) {
-        const double position = (double)a.positions[(int64_t)a.axis[j] * a.position_stride + token];
-        const double turns = position * (double)a.inv_freq[j] * 0.15915494309189535;  // 1 / (2 pi)
-        float s, c;
-        sincospif(2.0f * (float)(turns - __builtin_rint(turns)), &s, &c);
-        turn[j] = float2{c, s};
-    }
-    wave_fence();
-}
+// Cosines and sines of a token's pairs, a pair to a lane at a time (kPairs to a lane), in
+// the wave's own LDS.  The frequencies stay in registers from token to token, positions are
+// asked for ahead.
+template <int kPairs>
+struct Turns {
+    double freq[kPairs];  // turns for a position of 1
+    const int64_t *at[kPairs];
+    int64_t position[kPairs];
 
-// A lane's own pairs' cosines and sines (1 and 0 outside the turned part, where they are
-// not used).
-template <int V>
-__device__ __forceinline__ void read_turns(const float2 *turn, int32_t c, bool turned, float (&cs)[V], float (&sn)[V])
-{
+    __device__ __forceinline__ explicit Turns(const RopeArgs &a)
+    {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const float2 t = turned ? turn[c * V + e] : float2{1.0f, 0.0f};
-        cs[e] = t.x;
-        sn[e] = t.y;
+        for (int i = 0; i < kPairs; ++i) {
+            const int32_t j = (threadIdx.x & 63) + 64 * i;
+            const bool live = j < a.rot / 2;
+            freq[i] = live ? (double)a.inv_freq[j] * 0.15915494309189535 : 0.0;  // 1 / (2 pi)
+            at[i] = a.positions + (a.axes > 1 && live ? (int64_t)a.axis[j] * a.position_stride : 0);
+        }
     }
-}
 
+    __device__ __forceinline__ void ask(const RopeArgs &a, int64_t token)
+    {
+        if (a.rot > 0)
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i)
+                position[i] = load_global(at[i] + token);
+    }
+
+    __device__ __forceinline__ void write(const RopeArgs &a, float2 *turn) const
+    {
+        if (a.rot == 0)
+            return;
+        wave_fence();  // the token before has been read
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const double turns = (double)position[i] * freq[i];
+            float s, c;
+            sincospif(2.0f * (float)(turns - __builtin_rint(turns)), &s, &c);
+            turn[(threadIdx.x & 63) + 64 * i] = float2{c, s};
+        }
+        wave_fence();
+    }
+};
+
+// 1 / sqrt(mean + eps).  The hardware's reciprocal root is right to one unit in the last
+// place for all but subnormal arguments, which only an eps near 0 lets through.
 __device__ __forceinline__ float head_rstd(float squares, const RopeArgs &a)
 {
+    if (a.eps >= 0x1p-100f)
+        return __builtin_amdgcn_rsqf(__builtin_fmaf(squares, a.inv_dim, a.eps));
     return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(squares, (float)a.dim) + a.eps));
 }
 
-constexpr int kRopeThreads = 256;
+// Pairs to a lane when a wave takes a token's sines: rows of kLanes lanes of kChunks
+// chunks of V pairs.
+template <int V, int kLanes, int kChunks>
+constexpr int kPairsOf = (V * kLanes * kChunks + 63) / 64;
 
-// kSteps: steps (of 64 / kLanes heads of one tensor each) that a wave takes of a token;
-// kChunks: chunks of a row to a lane.
-template <typename T, int V, int kLanes, int kChunks, int kSteps>
-__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int32_t q_steps, int32_t steps, int32_t splits)
-{
-    __shared__ float2 turns[kRopeThreads / 64][kMaxPairs];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int32_t group = lane / kLanes;
-    constexpr int kHeads = 64 / kLanes;
+// What the waves of both passes share.  A step is 64 / kLanes heads of a token, a unit `per`
+// steps of one token; a wave takes every stride'th unit of one tensor.
+template <typename T, int V, int kLanes, int kChunks>
+struct HeadWave {
+    static constexpr int kHeads = 64 / kLanes;
+    const RopeArgs &a;
+    const HeadRows t;  // a copy: read from the arguments once, not at every step
+    const Selectors sel;
+    const int32_t group, steps, per, splits;
+    const int64_t stride, units;
+    const bool mixed;  // part of the row is not turned
     Chunk k[kChunks];
-    uint32_t w[2][kChunks][V];
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        k[i] = chunk_of<V>(lane % kLanes + i * 64, a);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-            load_pairs<V>(a.t[t].w, k[i], k[i].live && a.t[t].w, a.interleaved, w[t][i]);
-    }
-    const int64_t units = a.tokens * splits;
-    for (int64_t u = (int64_t)blockIdx.x * (kRopeThreads / 64) + wave; u < units;
-         u += (int64_t)gridDim.x * (kRopeThreads / 64)) {
-        const int64_t token = u / splits;
-        const int32_t first = (int32_t)(u - token * splits) * kSteps;
-        uint32_t x[kSteps][kChunks][V];
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const HeadRows &t = a.t[first + s >= q_steps];
-            const int32_t head = (first + s - (first + s >= q_steps ? q_steps : 0)) * kHeads + group;
-            const bool live = first + s < steps && head < t.heads;
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i)
-                load_pairs<V>(t.x + token * t.x_token + head * t.x_head, k[i], live && k[i].live, a.interleaved, x[s][i]);
-        }
-        float cs[kChunks][V], sn[kChunks][V];
-        if (a.rot > 0)
-            turn_pairs(a, token, turns[wave]);
+    float w[kChunks][2 * V];  // pairs, first and second element by turns; 1 without a weight
+
+    // A place in the wave's work: a step of a unit, up to step `end`.
+    struct Place {
+        int64_t unit, token;
+        int32_t step, end;
+    };
+
+    __device__ __forceinline__ HeadWave(const RopeArgs &args, int keys, int64_t stride_)
+        : a(args), t(args.t[keys]), sel(args), group((threadIdx.x & 63) / kLanes), steps((t.heads + kHeads - 1) / kHeads),
+          per(args.per[keys]), splits((steps + per - 1) / per), stride(stride_), units(args.tokens * splits),
+          mixed(args.rot < args.dim)
+    {
 #pragma unroll
         for (int i = 0; i < kChunks; ++i)
-            read_turns<V>(turns[wave], lane % kLanes + i * 64, k[i].turned, cs[i], sn[i]);
+            k[i] = chunk_of<V>((threadIdx.x & 63) % kLanes + i * 64, a);
+        Loaded<V, kChunks> l = {};
+        if (t.w)
+            l.load(t.w, Offsets<V, kChunks>(k, 0, 0), false);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            uint32_t p[V];
+            l.pairs(i, k[i], sel, p);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                w[i][2 * e] = t.w ? T::lo(p[e]) : 1.0f;
+                w[i][2 * e + 1] = t.w ? T::hi(p[e]) : 1.0f;
+            }
+        }
+    }
+
+    __device__ __forceinline__ int64_t token_of(int64_t unit) const { return splits == 1 ? unit : unit / splits; }
+
+    __device__ __forceinline__ Place place(int64_t unit) const
+    {
+        const int64_t token = token_of(unit);
+        const int32_t step = (int32_t)(unit - token * splits) * per;
+        return {unit, token, step, step + per < steps ? step + per : steps};
+    }
+
+    __device__ __forceinline__ Place next(const Place &p) const
+    {
+        return p.step + 1 < p.end ? Place{p.unit, p.token, p.step + 1, p.end} : place(p.unit + stride);
+    }
+
+    __device__ __forceinline__ bool has_head(const Place &p) const { return p.step * kHeads + group < t.heads; }
+
+    __device__ __forceinline__ int64_t at(const Place &p, int64_t token_stride, int64_t head_stride) const
+    {
+        return p.token * token_stride + (int64_t)p.step * kHeads * head_stride;
+    }
+
+    // A lane's own pairs' cosines and sines (1 and 0 outside the turned part).
+    __device__ __forceinline__ void read_turns(const float2 *turn, float (&cs)[kChunks][V], float (&sn)[kChunks][V]) const
+    {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int32_t c = k[i].turned ? (int32_t)(threadIdx.x & 63) % kLanes + i * 64 : 0;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float2 r = turn[pair_of<V>(c, e, a)];
+                cs[i][e] = r.x;
+                sn[i][e] = r.y;
+            }
+            if (mixed)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    cs[i][e] = k[i].turned ? cs[i][e] : 1.0f;
+                    sn[i][e] = k[i].turned ? sn[i][e] : 0.0f;
+                }
+        }
+    }
+};
+
+constexpr int kRopeThreads = 256;
+
+// Workgroups go round four tokens at a time: parts[0] of them take the queries' units, parts[1]
+// the keys', a wave one unit of at most kSteps steps of its token, so that a token's heads,
+// which lie together in memory, are read together.  The loads of all steps go out before
+// the sines are worked out.
+// With the weight multiplied into the cosines and sines once for the unit, an element of a
+// step costs three operations: out_a = (x_a rstd) (w_a cos) - (x_b rstd) (w_b sin).
+template <typename T, int V, int kLanes, int kChunks, int kSteps>
+__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a)
+{
+    constexpr int kWaves = kRopeThreads / 64;
+    __shared__ float2 turns[kWaves][64 * kPairsOf<V, kLanes, kChunks>];
+    typedef HeadWave<T, V, kLanes, kChunks> Wave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Turns<kPairsOf<V, kLanes, kChunks>> turn(a);
+    const int32_t splits = a.parts[0] + a.parts[1];
+    const int64_t blocks = (a.tokens + kWaves - 1) / kWaves * splits;
+    for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
+        const int64_t four = block / splits;
+        const int32_t split = (int32_t)(block - four * splits);
+        const int keys = split >= a.parts[0];
+        const Wave me(a, keys, 1);
+        const HeadRows &t = me.t;
+        const Offsets<V, kChunks> in(me.k, me.group, t.x_head), out(me.k, me.group, t.out_head);
+        const int64_t token = four * kWaves + wave;
+        if (token >= a.tokens)
+            continue;
+        turn.ask(a, token);
+        const int32_t first = (split - (keys ? a.parts[0] : 0)) * me.per;
+        const int32_t count = first + me.per < me.steps ? me.per : me.steps - first;
+        typename Wave::Place p{0, token, first, 0};
+        Loaded<V, kChunks> rows[kSteps];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+            if (s < count) {
+                p.step = first + s;
+                rows[s].load(t.x + me.at(p, t.x_token, t.x_head), in, !me.has_head(p));
+            }
+        turn.write(a, turns[wave]);
+        float ca[kChunks][V], sb[kChunks][V], cb[kChunks][V], sa[kChunks][V];
+        me.read_turns(turns[wave], ca, sb);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float wa = me.w[i][2 * e], wb = me.w[i][2 * e + 1];
+                cb[i][e] = ca[i][e] * wb;
+                sa[i][e] = sb[i][e] * wa;
+                ca[i][e] *= wa;
+                sb[i][e] *= wb;
+            }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int keys = first + s >= q_steps;
-            const HeadRows &t = a.t[keys];
-            const int32_t head = (first + s - (keys ? q_steps : 0)) * kHeads + group;
-            const bool live = first + s < steps && head < t.heads;
+            if (s >= count)
+                continue;
+            p.step = first + s;
+            float x[kChunks][2 * V];
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                uint32_t pair[V];
+                rows[s].pairs(i, me.k[i], me.sel, pair);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    x[i][2 * e] = T::lo(pair[e]);
+                    x[i][2 * e + 1] = T::hi(pair[e]);
+                }
+            }
             float rstd = 1.0f;
             if (t.w) {
                 float sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kChunks; ++i)
+                for (int i = 0; i < kChunks; ++i) {
+                    float part_sum = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        sum = __builtin_fmaf(T::lo(x[s][i][e]), T::lo(x[s][i][e]), sum);
-                        sum = __builtin_fmaf(T::hi(x[s][i][e]), T::hi(x[s][i][e]), sum);
-                    }
+                    for (int e = 0; e < 2 * V; ++e)
+                        part_sum = __builtin_fmaf(x[i][e], x[i][e], part_sum);
+                    sum += me.k[i].live ? part_sum : 0.0f;
+                }
                 rstd = head_rstd(lanes_sum<kLanes>(sum), a);
             }
+            uint16_t *to = t.out + me.at(p, t.out_token, t.out_head);
+            const bool live = me.has_head(p);
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 uint32_t o[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    float p = T::lo(x[s][i][e]), q = T::hi(x[s][i][e]);
-                    if (t.w) {
-                        const uint32_t we = keys ? w[1][i][e] : w[0][i][e];
-                        p = p * rstd * T::lo(we);
-                        q = q * rstd * T::hi(we);
-                    }
-                    const float pt = __builtin_fmaf(p, cs[i][e], -(q * sn[i][e]));
-                    const float qt = __builtin_fmaf(q, cs[i][e], p * sn[i][e]);
-                    o[e] = k[i].turned ? T::pack(pt, qt) : T::pack(p, q);
+                    float &xa = x[i][2 * e], &xb = x[i][2 * e + 1];
+                    xa *= rstd;
+                    xb *= rstd;
+                    o[e] = T::pack(__builtin_fmaf(xa, ca[i][e], -(xb * sb[i][e])),
+                                   __builtin_fmaf(xb, cb[i][e], xa * sa[i][e]));
                 }
-                if (live && k[i].live)
-                    store_pairs<V>(t.out + token * t.out_token + head * t.out_head, k[i], a.interleaved, o);
+                if (me.mixed) {  // no infinity of a pair's other half in what is not turned
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const uint32_t straight = T::pack(x[i][2 * e] * ca[i][e], x[i][2 * e + 1] * cb[i][e]);
+                        o[e] = me.k[i].turned ? o[e] : straight;
+                    }
+                }
+                if (live && me.k[i].live)
+                    store_pairs<V, kChunks>(to, out, i, me.k[i], me.sel, o);
             }
         }
     }
@@ -261,92 +489,114 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int32_t 
 
 // ------------------------------------------------------------------ backward --
 
-constexpr int kRopeGradThreads = 512;
+constexpr int kRopeGradThreads = 256;
 
-// Workgroups take parts: the first parts[0] queries', the others keys'; a wave of part p
-// takes every parts * 8'th token with all its heads, and sums the weight gradient of its
-// lanes' chunks over them.
+// Workgroups take sums: the first parts[0] the queries', the others the keys'; a wave of sum p
+// takes every parts * 4'th unit and sums the weight gradient of its lanes' chunks over them.
 template <typename T, int V, int kLanes, int kChunks>
 __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
 {
-    constexpr int kWaves = kRopeGradThreads / 64, kHeads = 64 / kLanes;
-    __shared__ float2 turns[kWaves][kMaxPairs];
-    __shared__ float sums[kWaves][ZR_MAX_HEAD_DIM];
+    constexpr int kWaves = kRopeGradThreads / 64;
+    __shared__ float2 turns[kWaves][64 * kPairsOf<V, kLanes, kChunks>];
+    __shared__ float sums[kWaves][2 * V * kLanes * kChunks];
+    typedef HeadWave<T, V, kLanes, kChunks> Wave;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    Chunk k[kChunks];
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-        k[i] = chunk_of<V>(lane % kLanes + i * 64, a);
-    for (int32_t part = blockIdx.x; part < a.parts[0] + a.parts[1]; part += gridDim.x) {
+    Turns<kPairsOf<V, kLanes, kChunks>> turn(a);
+    for (int64_t part = blockIdx.x; part < a.parts[0] + a.parts[1]; part += gridDim.x) {
         const int keys = part >= a.parts[0];
-        const HeadRows &t = a.t[keys];
-        const int32_t p = part - (keys ? a.parts[0] : 0), parts = a.parts[keys];
-        uint32_t w[kChunks][V];
+        const Wave me(a, keys, (int64_t)a.parts[keys] * kWaves);
+        const HeadRows &t = me.t;
+        const Offsets<V, kChunks> in(me.k, me.group, t.x_head), grad(me.k, me.group, t.dy_head),
+            out(me.k, me.group, t.out_head);
         float acc[kChunks][2 * V];
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            load_pairs<V>(t.w, k[i], k[i].live && t.w, a.interleaved, w[i]);
+        for (int i = 0; i < kChunks; ++i)
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e)
                 acc[i][e] = 0.0f;
+        Loaded<V, kChunks> dy = {}, xr = {};
+        const auto ask = [&](const typename Wave::Place &p) {
+            dy.load(t.dy + me.at(p, t.dy_token, t.dy_head), grad, !me.has_head(p));
+            if (t.w)
+                xr.load(t.x + me.at(p, t.x_token, t.x_head), in, !me.has_head(p));
+        };
+        typename Wave::Place p = me.place((part - (keys ? a.parts[0] : 0)) * kWaves + wave);
+        if (p.unit < me.units) {
+            turn.ask(a, p.token);
+            ask(p);
         }
-        for (int64_t token = (int64_t)p * kWaves + wave; token < a.tokens; token += (int64_t)parts * kWaves) {
-            float cs[kChunks][V], sn[kChunks][V];
-            if (a.rot > 0)
-                turn_pairs(a, token, turns[wave]);
+        float cs[kChunks][V], sn[kChunks][V];
+        for (int64_t turned = -1; p.unit < me.units;) {
+            if (p.unit != turned) {
+                turned = p.unit;
+                turn.write(a, turns[wave]);
+                me.read_turns(turns[wave], cs, sn);
+                if (p.unit + me.stride < me.units)
+                    turn.ask(a, me.token_of(p.unit + me.stride));
+            }
+            float g[kChunks][2 * V], x[kChunks][2 * V];
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i)
-                read_turns<V>(turns[wave], lane % kLanes + i * 64, k[i].turned, cs[i], sn[i]);
-            for (int32_t head = lane / kLanes; head - lane / kLanes < t.heads; head += kHeads) {
-                const bool live = head < t.heads;
-                uint32_t dy[kChunks][V], x[kChunks][V];
-                float g[kChunks][2 * V], squares = 0.0f, dot = 0.0f;
+            for (int i = 0; i < kChunks; ++i) {
+                uint32_t dw[V], xw[V];
+                dy.pairs(i, me.k[i], me.sel, dw);
+                xr.pairs(i, me.k[i], me.sel, xw);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float da = T::lo(dw[e]), db = T::hi(dw[e]);
+                    g[i][2 * e] = __builtin_fmaf(da, cs[i][e], db * sn[i][e]);
+                    g[i][2 * e + 1] = __builtin_fmaf(db, cs[i][e], -(da * sn[i][e]));
+                    x[i][2 * e] = T::lo(xw[e]);
+                    x[i][2 * e + 1] = T::hi(xw[e]);
+                }
+                if (me.mixed)  // no infinity of a pair's other half
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        g[i][2 * e] = me.k[i].turned ? g[i][2 * e] : T::lo(dw[e]);
+                        g[i][2 * e + 1] = me.k[i].turned ? g[i][2 * e + 1] : T::hi(dw[e]);
+                    }
+            }
+            const typename Wave::Place ahead = me.next(p);
+            if (ahead.unit < me.units)
+                ask(ahead);
+            const bool live = me.has_head(p);
+            if (t.w) {
+                float squares = 0.0f, dot = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
-                    load_pairs<V>(t.dy + token * t.dy_token + head * t.dy_head, k[i], live && k[i].live, a.interleaved, dy[i]);
-                    load_pairs<V>(t.x + token * t.x_token + head * t.x_head, k[i], live && k[i].live && t.w, a.interleaved,
-                                  x[i]);
+                    float sq = 0.0f, d = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 2 * V; ++e) {
+                        sq = __builtin_fmaf(x[i][e], x[i][e], sq);
+                        d = __builtin_fmaf(g[i][e] * x[i][e], me.w[i][e], d);
+                    }
+                    squares += me.k[i].live ? sq : 0.0f;
+                    dot += me.k[i].live ? d : 0.0f;
                 }
+                squares = lanes_sum<kLanes>(squares);
+                dot = lanes_sum<kLanes>(dot);
+                const float rstd = head_rstd(squares, a), along = dot * a.inv_dim * rstd * rstd;
+                // a head that is not there stands for the step's first: it adds nothing, and no
+                // NaN that the first does not add
+                const float counted = live ? rstd : 0.0f;
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float da = T::lo(dy[i][e]), db = T::hi(dy[i][e]);
-                        g[i][2 * e] = k[i].turned ? __builtin_fmaf(da, cs[i][e], db * sn[i][e]) : da;
-                        g[i][2 * e + 1] = k[i].turned ? __builtin_fmaf(db, cs[i][e], -(da * sn[i][e])) : db;
-                        const float xa = T::lo(x[i][e]), xb = T::hi(x[i][e]);
-                        squares = __builtin_fmaf(xa, xa, squares);
-                        squares = __builtin_fmaf(xb, xb, squares);
-                        dot = __builtin_fmaf(g[i][2 * e] * T::lo(w[i][e]), xa, dot);
-                        dot = __builtin_fmaf(g[i][2 * e + 1] * T::hi(w[i][e]), xb, dot);
+                    for (int e = 0; e < 2 * V; ++e) {
+                        acc[i][e] = __builtin_fmaf(g[i][e] * x[i][e], counted, acc[i][e]);
+                        g[i][e] = __builtin_fmaf(-along, x[i][e], g[i][e] * me.w[i][e]) * rstd;
                     }
-                if (t.w) {
-                    squares = lanes_sum<kLanes>(squares);
-                    dot = lanes_sum<kLanes>(dot);
-                    const float rstd = head_rstd(squares, a);
-                    const float along = __fdiv_rn(dot, (float)a.dim) * rstd * rstd;
-#pragma unroll
-                    for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            const float xa = T::lo(x[i][e]), xb = T::hi(x[i][e]);
-                            float &ga = g[i][2 * e], &gb = g[i][2 * e + 1];
-                            acc[i][2 * e] = __builtin_fmaf(ga, live ? xa * rstd : 0.0f, acc[i][2 * e]);
-                            acc[i][2 * e + 1] = __builtin_fmaf(gb, live ? xb * rstd : 0.0f, acc[i][2 * e + 1]);
-                            ga = __builtin_fmaf(-along, xa, ga * T::lo(w[i][e])) * rstd;
-                            gb = __builtin_fmaf(-along, xb, gb * T::hi(w[i][e])) * rstd;
-                        }
-                }
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    uint32_t o[V];
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        o[e] = T::pack(g[i][2 * e], g[i][2 * e + 1]);
-                    if (live && k[i].live)
-                        store_pairs<V>(t.out + token * t.out_token + head * t.out_head, k[i], a.interleaved, o);
-                }
             }
+            uint16_t *to = t.out + me.at(p, t.out_token, t.out_head);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                uint32_t o[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    o[e] = T::pack(g[i][2 * e], g[i][2 * e + 1]);
+                if (live && me.k[i].live)
+                    store_pairs<V, kChunks>(to, out, i, me.k[i], me.sel, o);
+            }
+            p = ahead;
         }
         if (!t.w)
             continue;
@@ -358,11 +608,8 @@ __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
 #pragma unroll
                 for (int m = kLanes; m < 64; m *= 2)
                     acc[i][e] += __shfl_xor(acc[i][e], m, 64);
-                const bool b = e & 1;
-                const int32_t at = a.interleaved || V == 1 ? k[i].first + e : (b ? k[i].other : k[i].first) + e / 2;
-                const int32_t column = V == 1 && b ? k[i].other : at;
-                if (lane < kLanes && k[i].live && column < a.dim)
-                    sums[wave][column] = acc[i][e];
+                if (lane < kLanes && me.k[i].live && (V > 1 || e == 0 || me.k[i].second))
+                    sums[wave][column_of<V>(me.k[i], e / 2, e % 2, a)] = acc[i][e];
             }
         __syncthreads();
         for (int32_t c = threadIdx.x; c < a.dim; c += kRopeGradThreads) {
@@ -370,7 +617,7 @@ __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
 #pragma unroll
             for (int i = 1; i < kWaves; ++i)
                 sum += sums[i][c];
-            a.partial[(int64_t)part * a.dim + c] = sum;
+            a.partial[part * a.dim + c] = sum;
         }
         __syncthreads();
     }
@@ -378,8 +625,14 @@ __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
 
 // Weight gradients from the partial sums: a workgroup takes 32 columns of one tensor, 16
 // threads to a column, each every 16th partial sum; they meet in LDS in that order.
+// Partial sums that a call makes, at most: two workgroups to a compute unit.
+constexpr int64_t kGradParts = 512;
+static_assert(kGradParts <= ZR_QK_PARTIALS, "the workspace holds them");
+
+constexpr int kDweightThreads = 512;
+
 template <typename T>
-__global__ __launch_bounds__(kRopeGradThreads) void rope_dweight_kernel(const float *partial, int32_t dim, int32_t q_parts,
+__global__ __launch_bounds__(kDweightThreads) void rope_dweight_kernel(const float *partial, int32_t dim, int32_t q_parts,
                                                                         int32_t k_parts, uint16_t *dq, uint16_t *dk)
 {
     __shared__ float part[16][33];
@@ -520,64 +773,114 @@ void fill_args(RopeArgs *a, int64_t tokens, int64_t head_dim, double eps, const 
     a->partial = nullptr;
     a->dim = (int32_t)head_dim;
     a->rot = rope->rot_dim;
+    a->axes = rope->pair_axis ? rope->axes : 1;
     a->interleaved = rope->interleaved;
     a->parts[0] = a->parts[1] = 0;
+    a->per[0] = a->per[1] = 1;
     a->eps = (float)eps;
+    a->inv_dim = 1.0f / (float)head_dim;
     for (int32_t j = 0; j < kMaxPairs; ++j)
         a->axis[j] = rope->pair_axis && j < rope->rot_dim / 2 ? rope->pair_axis[j] : 0;
 }
 
-template <typename T, int V, int kLanes, int kChunks>
-zr_status rope_launch(const RopeArgs &a, hipStream_t st)
-{
-    constexpr int heads = 64 / kLanes, kSteps = 4;
-    const int32_t q_steps = (a.t[0].heads + heads - 1) / heads, steps = q_steps + (a.t[1].heads + heads - 1) / heads;
-    const int32_t splits = (steps + kSteps - 1) / kSteps;
-    const int64_t units = a.tokens * splits;
-    return launch(rope_kernel<T, V, kLanes, kChunks, kSteps>, grid_of((units + 3) / 4), dim3(kRopeThreads), 0, st, a,
-                  q_steps, steps, splits);
-}
+constexpr int64_t kFewSteps = 2048;
 
-template <typename T, int V, int kLanes, int kChunks>
-zr_status rope_grad_launch(const RopeArgs &a, hipStream_t st)
+template <typename T, int V, int kLanes, int kChunks, int kSteps>
+zr_status rope_steps(RopeArgs *a, hipStream_t st)
 {
-    return launch(rope_grad_kernel<T, V, kLanes, kChunks>, grid_of(a.parts[0] + a.parts[1]), dim3(kRopeGradThreads), 0, st,
-                  a);
-}
-
-// Calls F with the layout of a row: vectors of 8 or 4 elements where both halves of the
-// turned part and the rest are whole chunks, else single elements.
-template <typename T, template <typename, int, int, int> class F>
-zr_status for_layout(const RopeArgs &a, hipStream_t st)
-{
-    const int32_t rest = a.dim - a.rot;
-    if (a.rot % 16 == 0 && rest % 16 == 0) {
-        if (a.dim <= 64)
-            return F<T, 8, 4, 1>::run(a, st);
-        if (a.dim <= 128)
-            return F<T, 8, 8, 1>::run(a, st);
-        if (a.dim <= 256)
-            return F<T, 8, 16, 1>::run(a, st);
-        return F<T, 8, 32, 1>::run(a, st);
+    constexpr int kHeads = 64 / kLanes, kWaves = kRopeThreads / 64;
+    for (int t = 0; t < 2; ++t) {
+        const int64_t steps = (a->t[t].heads + kHeads - 1) / kHeads, splits = (steps + kSteps - 1) / kSteps;
+        a->per[t] = splits > 0 ? (int32_t)((steps + splits - 1) / splits) : 1;
+        a->parts[t] = (int32_t)((steps + a->per[t] - 1) / a->per[t]);
     }
-    if (a.rot % 8 == 0 && rest % 8 == 0) {
-        if (a.dim <= 128)
-            return F<T, 4, 16, 1>::run(a, st);
-        return F<T, 4, 64, 1>::run(a, st);
-    }
-    if (a.dim <= 128)
-        return F<T, 1, 64, 1>::run(a, st);
-    return F<T, 1, 64, 4>::run(a, st);
+    const int64_t blocks = (a->tokens + kWaves - 1) / kWaves * (a->parts[0] + a->parts[1]);
+    return launch(rope_kernel<T, V, kLanes, kChunks, kSteps>, grid_of(blocks), dim3(kRopeThreads), 0, st, *a);
 }
 
+// Few tokens: a wave to a step, for latency.  Else a unit is a token's steps, four at most.
 template <typename T, int V, int kLanes, int kChunks>
-struct Forward {
-    static zr_status run(const RopeArgs &a, hipStream_t st) { return rope_launch<T, V, kLanes, kChunks>(a, st); }
-};
+zr_status rope_launch(RopeArgs *a, hipStream_t st)
+{
+    constexpr int kHeads = 64 / kLanes;
+    const int64_t steps = (a->t[0].heads + kHeads - 1) / kHeads + (a->t[1].heads + kHeads - 1) / kHeads;
+    return a->tokens * steps <= kFewSteps ? rope_steps<T, V, kLanes, kChunks, 1>(a, st)
+                                          : rope_steps<T, V, kLanes, kChunks, 4>(a, st);
+}
+
+// Steps of a unit, at most: its waves take the sines once for them, and all waves end within
+// a unit of one another.
+constexpr int64_t kUnitSteps = 2;
+
+// Parts go to the tensors by their heads; units are smaller where they would be too few to
+// give every wave one.
 template <typename T, int V, int kLanes, int kChunks>
-struct Backward {
-    static zr_status run(const RopeArgs &a, hipStream_t st) { return rope_grad_launch<T, V, kLanes, kChunks>(a, st); }
-};
+zr_status rope_grad_launch(RopeArgs *a, hipStream_t st)
+{
+    constexpr int kHeads = 64 / kLanes, kWaves = kRopeGradThreads / 64;
+    const int64_t heads = (int64_t)a->t[0].heads + a->t[1].heads;
+    for (int t = 0; t < 2; ++t)
+        if (a->t[t].heads > 0) {
+            int64_t share = kGradParts * a->t[t].heads / heads;
+            share = share < 1 ? 1 : share > kGradParts - 1 && a->t[1 - t].heads > 0 ? kGradParts - 1 : share;
+            const int64_t steps = (a->t[t].heads + kHeads - 1) / kHeads, waves = share * kWaves;
+            int64_t splits = (waves + a->tokens - 1) / a->tokens;
+            splits = splits > (steps + kUnitSteps - 1) / kUnitSteps ? splits : (steps + kUnitSteps - 1) / kUnitSteps;
+            splits = splits < steps ? splits : steps;
+            a->per[t] = (int32_t)((steps + splits - 1) / splits);
+            const int64_t units = a->tokens * ((steps + a->per[t] - 1) / a->per[t]), most = (units + kWaves - 1) / kWaves;
+            a->parts[t] = (int32_t)(share < most ? share : most);
+        }
+    return launch(rope_grad_kernel<T, V, kLanes, kChunks>, grid_of(a->parts[0] + a->parts[1]), dim3(kRopeGradThreads), 0,
+                  st, *a);
+}
+
+// The layout of a row: vectors of 8 or 4 (2) elements where both halves of the turned part
+// and of the rest are whole vectors, else single elements; as many lanes as its chunks need.
+// Forward, vectors of 4 leave room for 7 waves to a SIMD where those of 8 leave 4 (5003
+// tokens of 24 heads of 96: 12.4 us and 14.9; 16384 of 40 of 128: 57.7 and 57.3); backward,
+// where sums stay in registers anyway, 8 need half as many steps (118 us and 99).
+template <typename T, bool kForward, int V, int kLanes, int kChunks>
+zr_status layout_launch(RopeArgs *a, hipStream_t st)
+{
+    if constexpr (kForward)
+        return rope_launch<T, V, kLanes, kChunks>(a, st);
+    else
+        return rope_grad_launch<T, V, kLanes, kChunks>(a, st);
+}
+
+template <typename T, bool kForward>
+zr_status for_layout(RopeArgs *a, hipStream_t st)
+{
+    const int32_t rest = a->dim - a->rot;
+    if constexpr (!kForward)
+        if (a->rot % 16 == 0 && rest % 16 == 0) {
+            if (a->dim <= 64)
+                return layout_launch<T, kForward, 8, 4, 1>(a, st);
+            if (a->dim <= 128)
+                return layout_launch<T, kForward, 8, 8, 1>(a, st);
+            if (a->dim <= 256)
+                return layout_launch<T, kForward, 8, 16, 1>(a, st);
+            return layout_launch<T, kForward, 8, 32, 1>(a, st);
+        }
+    if (a->rot % 8 == 0 && rest % 8 == 0) {
+        if (a->dim <= 64)
+            return layout_launch<T, kForward, 4, 8, 1>(a, st);
+        if (a->dim <= 128)
+            return layout_launch<T, kForward, 4, 16, 1>(a, st);
+        if (a->dim <= 256)
+            return layout_launch<T, kForward, 4, 32, 1>(a, st);
+        return layout_launch<T, kForward, 4, 64, 1>(a, st);
+    }
+    if (a->rot % 4 == 0 && rest % 4 == 0) {
+        if (a->dim <= 128)
+            return layout_launch<T, kForward, 2, 32, 1>(a, st);
+        return layout_launch<T, kForward, 2, 64, 2>(a, st);
+    }
+    if (a->dim <= 128)
+        return layout_launch<T, kForward, 1, 64, 1>(a, st);
+    return layout_launch<T, kForward, 1, 64, 4>(a, st);
+}
 
 int64_t heads_of(const zr_heads *h) { return h ? h->heads : 0; }
 bool same_heads(const zr_heads *a, const zr_heads *b)
@@ -632,7 +935,7 @@ extern "C" zr_status zr_qk_norm_rope(const zr_heads *q, const zr_heads *k, const
                   static_cast<uint16_t *>(out[t]->ptr), in[t]->token_stride, in[t]->head_stride, 0, 0,
                   out[t]->token_stride, out[t]->head_stride, (int32_t)in[t]->heads};
     const auto st = static_cast<hipStream_t>(stream);
-    return dtype == ZR_BF16 ? for_layout<BF16, Forward>(a, st) : for_layout<F16, Forward>(a, st);
+    return dtype == ZR_BF16 ? for_layout<BF16, true>(&a, st) : for_layout<F16, true>(&a, st);
 }
 
 extern "C" zr_status zr_qk_norm_rope_backward(const zr_heads *dq, const zr_heads *dk, const zr_heads *q, const zr_heads *k,
@@ -696,23 +999,15 @@ extern "C" zr_status zr_qk_norm_rope_backward(const zr_heads *dq, const zr_heads
                   static_cast<const uint16_t *>(w[t]), static_cast<uint16_t *>(out[t]->ptr), x[t]->token_stride,
                   x[t]->head_stride, dy[t]->token_stride, dy[t]->head_stride, out[t]->token_stride, out[t]->head_stride,
                   (int32_t)dy[t]->heads};
-    // parts go to the tensors by their heads, at most one to 8 tokens
-    const int64_t most = (tokens + 7) / 8, heads = a.t[0].heads + a.t[1].heads;
-    for (int t = 0; t < 2; ++t)
-        if (a.t[t].heads > 0) {
-            int64_t share = ZR_QK_PARTIALS * a.t[t].heads / heads;
-            share = share < 1 ? 1 : share > ZR_QK_PARTIALS - 1 && a.t[1 - t].heads > 0 ? ZR_QK_PARTIALS - 1 : share;
-            a.parts[t] = (int32_t)(share < most ? share : most);
-        }
     const auto st = static_cast<hipStream_t>(stream);
-    if (a.parts[0] + a.parts[1] > 0) {
-        s = dtype == ZR_BF16 ? for_layout<BF16, Backward>(a, st) : for_layout<F16, Backward>(a, st);
+    if (a.t[0].heads + a.t[1].heads > 0) {
+        s = dtype == ZR_BF16 ? for_layout<BF16, false>(&a, st) : for_layout<F16, false>(&a, st);
         if (s != ZR_OK)
             return s;
     }
     if (!dq_weight && !dk_weight)
         return ZR_OK;
-    const dim3 grid = grid_of(2 * ((head_dim + 31) / 32)), block(kRopeGradThreads);
+    const dim3 grid = grid_of(2 * ((head_dim + 31) / 32)), block(kDweightThreads);
     const auto gq = static_cast<uint16_t *>(dq_weight), gk = static_cast<uint16_t *>(dk_weight);
     return dtype == ZR_BF16 ? launch(rope_dweight_kernel<BF16>, grid, block, 0, st, (const float *)workspace, a.dim, a.parts[0], a.parts[1], gq, gk)
                             : launch(rope_dweight_kernel<F16>, grid, block, 0, st, (const float *)workspace, a.dim, a.parts[0], a.parts[1], gq, gk);
