@@ -22,8 +22,13 @@ def at(i, off=0):
     return A + i * (1 << 40) + off
 
 
+class Heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("heads", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 def heads(i, n, off=0, token=None, head=D):
-    return zr._Heads(at(i, off), n, n * D if token is None else token, head)
+    return Heads(at(i, off), n, n * D if token is None else token, head)
 
 
 def rope(rot=D, axes=1, axis=None, interleaved=0, inv_freq=at(8)):
@@ -66,7 +71,7 @@ BOTH = [
     (dict(rope=rope(inv_freq=None)), 1), (dict(rope=rope(inv_freq=at(8, 2))), 3), (dict(positions=None), 1),
     (dict(positions=at(4, 4)), 3), (dict(rope=rope(axes=2), position_stride=T - 1), 1),
     (dict(rope=rope(axes=2), position_stride=1 << 61), 1), (dict(q_weight=at(2, 1)), 3), (dict(k_weight=at(3, 1)), 3),
-    (dict(q=None), 1), (dict(k=zr._Heads(None, HK, HK * D, D)), 1), (dict(q=heads(0, HQ, off=1)), 3),
+    (dict(q=None), 1), (dict(k=Heads(None, HK, HK * D, D)), 1), (dict(q=heads(0, HQ, off=1)), 3),
     (dict(q=heads(0, HQ, token=HQ * D - 1)), 1), (dict(q=heads(0, HQ, head=D - 1)), 1), (dict(q=heads(0, HQ, token=-64)), 1),
     (dict(q=heads(0, HQ, token=1 << 62)), 1), (dict(q=heads(0, HQ, head=1 << 62)), 1),
     (dict(q=heads(0, HQ, token=D, head=T * D - 1)), 1), (dict(q=heads(0, HQ, token=0, head=0)), 1)]
@@ -87,7 +92,7 @@ def test_forward_refusals(change, code):
 
 
 @pytest.mark.parametrize("change,code", BOTH + [
-    (dict(dq=zr._Heads(None, HQ, HQ * D, D)), 1), (dict(dk_in=None), 1), (dict(dq_weight=None), 1), (dict(dk_weight=None), 1),
+    (dict(dq=Heads(None, HQ, HQ * D, D)), 1), (dict(dk_in=None), 1), (dict(dq_weight=None), 1), (dict(dk_weight=None), 1),
     (dict(workspace=None), 1), (dict(dq_weight=at(12, 1)), 3), (dict(workspace=at(14, 2)), 3), (dict(q=heads(0, HQ - 1)), 1),
     (dict(dq=heads(10, 65537)), 1), (dict(dk_weight=at(12, 2)), 1), (dict(dq_weight=at(14)), 1), (dict(dq_weight=at(2)), 1),
     (dict(dq_in=heads(14, HQ)), 1), (dict(dq_in=heads(10, HQ, off=2)), 1), (dict(dq_in=heads(1, HQ)), 1),
@@ -98,7 +103,7 @@ def test_backward_refusals(change, code):
 
 
 def test_calls_without_work():
-    none = zr._Heads(None, 0, 0, 0)
+    none = Heads(None, 0, 0, 0)
     assert call("zr_qk_norm_rope", FORWARD, tokens=0) == 0
     assert call("zr_qk_norm_rope", FORWARD, tokens=0, q=None, k=None, positions=None, q_out=None, k_out=None) == 0
     assert call("zr_qk_norm_rope", FORWARD, q=None, k=none, q_out=None, k_out=None) == 0

@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import List, Optional, Sequence, Tuple, Union
 
 import torch  # loads the process's HIP runtime before libzr binds to it
@@ -79,11 +80,6 @@ class _HParams(ctypes.Structure):
 
 class _ClipHParams(ctypes.Structure):
     _fields_ = [("max_norm", ctypes.c_double), ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double)]
-
-
-class _Heads(ctypes.Structure):
-    _fields_ = [("ptr", ctypes.c_void_p), ("heads", ctypes.c_int64), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64)]
 
 
 class _Rope(ctypes.Structure):
@@ -935,7 +931,7 @@ def zr_adamw_step_clip(grad: torch.Tensor, master: torch.Tensor, exp_avg: torch.
                   int(step))
     numel = master.numel() if numel is None else int(numel)
     _need(numel, grad=grad, master=master, exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, param_out=param_out)
-    _gpu_call(_lib.zr_adamw_step_clip, stream, (grad, master, exp_avg, exp_avg_sq, param_out, clip),
+    _gpu_call_flat(_lib.zr_adamw_step_clip, stream, (grad, master, exp_avg, exp_avg_sq, param_out, clip),
               _ptr(grad, 2, "grad"), _ptr(master, 4, "master"), _ptr(exp_avg, 4, "exp_avg"),
               _ptr(exp_avg_sq, 4, "exp_avg_sq"), _ptr(param_out, 2, "param_out"), numel, ctypes.byref(hp), _clip(clip))
 
@@ -949,7 +945,7 @@ def zr_adamw_step_clip_f16(grad: torch.Tensor, master: torch.Tensor, exp_avg: to
                   int(step))
     numel = master.numel() if numel is None else int(numel)
     _need(numel, grad=grad, master=master, exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, param_out=param_out)
-    _gpu_call(_lib.zr_adamw_step_clip_f16, stream, (grad, master, exp_avg, exp_avg_sq, param_out, ls, clip),
+    _gpu_call_flat(_lib.zr_adamw_step_clip_f16, stream, (grad, master, exp_avg, exp_avg_sq, param_out, ls, clip),
               _ptr(grad, 2, "grad"), _ptr(master, 4, "master"), _ptr(exp_avg, 4, "exp_avg"),
               _ptr(exp_avg_sq, 4, "exp_avg_sq"), _ptr(param_out, 2, "param_out"), numel, ctypes.byref(hp), _ls(ls),
               _clip(clip))
@@ -960,6 +956,9 @@ def zr_adamw_step_clip_f16(grad: torch.Tensor, master: torch.Tensor, exp_avg: to
 ZR_MAX_HEAD_DIM = 512
 ZR_MAX_ROPE_AXES = 4
 ZR_QK_PARTIALS = 512
+
+
+_HEADS = struct.Struct("4q")  # zr_heads
 
 
 class Rope:
@@ -979,6 +978,7 @@ class Rope:
         self._axis = (ctypes.c_uint8 * max(1, half))(*axis) if axis is not None else None
         self.c = _Rope(p, None if axis is None else ctypes.addressof(self._axis), 2 * half, self.axes,
                        int(bool(interleaved)))
+        self.ref = ctypes.byref(self.c)
 
 
 def rope(inv_freq: torch.Tensor, *, interleaved: bool = False, pair_axis: Optional[Sequence[int]] = None) -> Rope:
@@ -993,23 +993,24 @@ def qk_norm_workspace(head_dim: int, device=None) -> torch.Tensor:
     return torch.empty(ZR_QK_PARTIALS, head_dim, dtype=torch.float32, device=device if device is not None else "cuda")
 
 
-def _heads(t: Optional[torch.Tensor], dtype, name: str, shape=None):
-    """A tensor [tokens, heads, head_dim] with contiguous rows as a zr_heads (None for None)."""
+def _heads(t: Optional[torch.Tensor], dtype, tokens: int, heads: Optional[int], dim: int, name: str):
+    """A tensor [tokens, heads, dim] with contiguous rows (heads None: any) as the bytes of a
+    zr_heads, and its heads; (None, 0) for None."""
     if t is None:
-        return None
+        return None, 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    own = t.shape
-    if len(own) != 3:
+    shape, strides = t.shape, t.stride()
+    if len(strides) != 3:
         raise ValueError(f"{name} must have three dimensions: tokens, heads, head_dim")
+    n, h, d = shape
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and own != shape:
-        raise ValueError(f"{name} is {tuple(own)}, {tuple(shape)} needed")
-    strides = t.stride()
-    if own[2] > 1 and strides[2] != 1:
+    if n != tokens or d != dim or (heads is not None and h != heads):
+        raise ValueError(f"{name} is {n} x {h} x {d}, {tokens} x {'any' if heads is None else heads} x {dim} needed")
+    if strides[2] != 1 and d > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return _Heads(t.data_ptr() or None, own[1], strides[0], strides[1])
+    return _HEADS.pack(t.data_ptr(), h, strides[0], strides[1]), h
 
 
 def _positions(positions: Optional[torch.Tensor], tokens: int, axes: int):
@@ -1021,15 +1022,15 @@ def _positions(positions: Optional[torch.Tensor], tokens: int, axes: int):
     if positions.dtype != torch.int64:
         raise TypeError(f"positions must be torch.int64, not {positions.dtype}")
     shape, strides = positions.shape, positions.stride()
-    if (shape != (tokens,) or axes > 1) and (len(shape) != 2 or shape[0] < axes or shape[1] != tokens):
+    if axes == 1 and shape == (tokens,):
+        if tokens > 1 and strides[0] != 1:
+            raise ValueError("positions must be contiguous along the tokens")
+        return positions.data_ptr() or None, tokens
+    if len(shape) != 2 or shape[0] < axes or shape[1] != tokens:
         raise ValueError(f"positions is {tuple(shape)}, {(axes, tokens) if axes > 1 else (tokens,)} needed")
     if tokens > 1 and strides[-1] != 1:
         raise ValueError("positions must be contiguous along the tokens")
-    return positions.data_ptr() or None, strides[0] if len(shape) == 2 else tokens
-
-
-def _ref(c):
-    return None if c is None else ctypes.byref(c)
+    return positions.data_ptr() or None, strides[0]
 
 
 def _qk(q, k):
@@ -1040,11 +1041,10 @@ def _qk(q, k):
     if not isinstance(one, torch.Tensor):
         raise TypeError("q and k must be torch.Tensors")
     _typed(one, (torch.bfloat16, torch.float16), "q and k")
-    if len(one.shape) != 3:
+    shape = one.shape
+    if len(shape) != 3:
         raise ValueError("q and k must have three dimensions: tokens, heads, head_dim")
-    if q is not None and k is not None and (len(k.shape) != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]):
-        raise ValueError(f"q is {tuple(q.shape)} and k {tuple(k.shape)}: tokens and head_dim must agree")
-    return one.dtype, one.shape[0], one.shape[2]
+    return one.dtype, shape[0], shape[2]
 
 
 def zr_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
@@ -1057,14 +1057,12 @@ def zr_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weig
     may be q, k_out k.  Tokens and heads may have any strides (slices of the fused
     product's rows)."""
     kind, tokens, dim = _qk(q, k)
-    c_q, c_k = _heads(q, kind, "q"), _heads(k, kind, "k")
-    c_qo = _heads(q_out, kind, "q_out", q.shape if q is not None else None)
-    c_ko = _heads(k_out, kind, "k_out", k.shape if k is not None else None)
+    (c_q, hq), (c_k, hk) = _heads(q, kind, tokens, None, dim, "q"), _heads(k, kind, tokens, None, dim, "k")
+    c_qo, c_ko = _heads(q_out, kind, tokens, hq, dim, "q_out")[0], _heads(k_out, kind, tokens, hk, dim, "k_out")[0]
     p_pos, stride = _positions(positions, tokens, rope.axes)
     p_qw, p_kw = _vector(q_weight, (kind,), dim, "q_weight"), _vector(k_weight, (kind,), dim, "k_weight")
     _gpu_call_flat(_lib.zr_qk_norm_rope, stream, (q, k, q_weight, k_weight, positions, rope.inv_freq, q_out, k_out),
-                   _ref(c_q), _ref(c_k), p_qw, p_kw, _DTYPES[kind], tokens, dim, float(eps), p_pos, stride,
-                   ctypes.byref(rope.c), _ref(c_qo), _ref(c_ko))
+                   c_q, c_k, p_qw, p_kw, _DTYPES[kind], tokens, dim, float(eps), p_pos, stride, rope.ref, c_qo, c_ko)
 
 
 def zr_qk_norm_rope_backward(dq: Optional[torch.Tensor], dk: Optional[torch.Tensor], q: Optional[torch.Tensor],
@@ -1078,10 +1076,9 @@ def zr_qk_norm_rope_backward(dq: Optional[torch.Tensor], dk: Optional[torch.Tens
     forward pass's inputs (not read, and may be None, without a weight).  dq_in may be dq or
     q, dk_in dk or k."""
     kind, tokens, dim = _qk(dq, dk)
-    shape_q, shape_k = dq.shape if dq is not None else None, dk.shape if dk is not None else None
-    c_dq, c_dk = _heads(dq, kind, "dq"), _heads(dk, kind, "dk")
-    c_q, c_k = _heads(q, kind, "q", shape_q), _heads(k, kind, "k", shape_k)
-    c_qi, c_ki = _heads(dq_in, kind, "dq_in", shape_q), _heads(dk_in, kind, "dk_in", shape_k)
+    (c_dq, hq), (c_dk, hk) = _heads(dq, kind, tokens, None, dim, "dq"), _heads(dk, kind, tokens, None, dim, "dk")
+    c_q, c_k = _heads(q, kind, tokens, hq, dim, "q")[0], _heads(k, kind, tokens, hk, dim, "k")[0]
+    c_qi, c_ki = _heads(dq_in, kind, tokens, hq, dim, "dq_in")[0], _heads(dk_in, kind, tokens, hk, dim, "dk_in")[0]
     p_pos, stride = _positions(positions, tokens, rope.axes)
     p_qw, p_kw = _vector(q_weight, (kind,), dim, "q_weight"), _vector(k_weight, (kind,), dim, "k_weight")
     p_dqw, p_dkw = _vector(dq_weight, (kind,), dim, "dq_weight"), _vector(dk_weight, (kind,), dim, "dk_weight")
@@ -1089,5 +1086,5 @@ def zr_qk_norm_rope_backward(dq: Optional[torch.Tensor], dk: Optional[torch.Tens
     _gpu_call_flat(_lib.zr_qk_norm_rope_backward, stream,
                    (dq, dk, q, k, q_weight, k_weight, positions, rope.inv_freq, dq_in, dk_in, dq_weight, dk_weight,
                     workspace),
-                   _ref(c_dq), _ref(c_dk), _ref(c_q), _ref(c_k), p_qw, p_kw, _DTYPES[kind], tokens, dim, float(eps),
-                   p_pos, stride, ctypes.byref(rope.c), _ref(c_qi), _ref(c_ki), p_dqw, p_dkw, p_ws)
+                   c_dq, c_dk, c_q, c_k, p_qw, p_kw, _DTYPES[kind], tokens, dim, float(eps), p_pos, stride, rope.ref,
+                   c_qi, c_ki, p_dqw, p_dkw, p_ws)

@@ -441,10 +441,12 @@ zr_status check_list(const char *who, const void *const *grads, const int64_t *n
     return ZR_OK;
 }
 
-// Calls run(batch) for the non-empty tensors, kMaxPieces at a time.  kLines: a tensor's
-// first tile starts on the 128-byte line that holds its first element (the descriptor
-// keeps the element's own address).
-template <bool kLines, typename F>
+// Calls run(batch) for the non-empty tensors, kMaxPieces at a time.  kInPlace (scaling, where
+// neither order nor bounds of the tensors matter): a tensor that starts where the one before
+// it ends goes on as one piece with it, as the tensors of a flat buffer do, and a piece's first
+// tile starts on the 128-byte line that holds its first element (the table keeps the
+// element's own address).
+template <bool kInPlace, typename F>
 zr_status for_batches(const void *const *grads, const int64_t *numels, int32_t n, int64_t size, F run)
 {
     PieceBatch batch;
@@ -456,11 +458,18 @@ zr_status for_batches(const void *const *grads, const int64_t *numels, int32_t n
         batch.tiles = 0;
         return s;
     };
-    for (int32_t t = 0; t < n; ++t) {
-        if (numels[t] == 0)
+    for (int32_t t = 0; t < n;) {
+        if (numels[t] == 0) {
+            ++t;
             continue;
+        }
         const uintptr_t p = reinterpret_cast<uintptr_t>(grads[t]);
-        const int64_t bytes = size * numels[t] + (kLines ? (int64_t)(p & 127) : 0);
+        int64_t bytes = size * numels[t++];
+        if constexpr (kInPlace) {
+            for (; t < n && (numels[t] == 0 || reinterpret_cast<uintptr_t>(grads[t]) == p + (uintptr_t)bytes); ++t)
+                bytes += size * numels[t];
+            bytes += (int64_t)(p & 127);
+        }
         const int64_t tiles = (bytes + kTileBytes - 1) / kTileBytes;
         if (batch.count == kMaxPieces || batch.tiles + tiles > 0xfffffff0) {
             const zr_status s = flush();
