@@ -174,7 +174,8 @@ def check_backward(c, eps=1e-5, in_place=None):
 
 DIMS = [(128, 128), (128, 64), (128, 32), (64, 64), (96, 96), (80, 80), (80, 20), (72, 72), (88, 40), (256, 256), (256, 64),
         (512, 512), (512, 128), (200, 200), (40, 40), (16, 16), (2, 2), (6, 4), (7, 6), (1, 0), (33, 18), (127, 126), (129, 128),
-        (511, 510), (300, 298), (128, 0), (50, 50), (130, 130)]
+        (511, 510), (300, 298), (128, 0), (50, 50), (130, 130), (512, 510), (509, 0), (127, 8), (511, 500), (66, 66), (80, 18),
+        (300, 2), (512, 6), (24, 8), (23, 16), (9, 8), (8, 6), (17, 16), (31, 14), (260, 256), (130, 0), (5, 0), (3, 2)]
 
 
 @pytest.mark.parametrize("dtype", [BF, FP16])

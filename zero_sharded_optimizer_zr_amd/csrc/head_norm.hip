@@ -12,6 +12,8 @@
 // they are neighbours the loaded words are the pairs.  A wave works on 64 / kGroupLanes
 // heads of one token at a time, so that a token's sines and cosines, taken once by the
 // wave (a lane to a pair) and handed over through LDS, serve all its heads.
+#include <algorithm>
+
 #include "fp8.hpp"
 #include "zr_rope.h"
 
@@ -51,42 +53,63 @@ template <>
 struct Vec<4> {
     typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2)));
 };
-template <>
-struct Vec<2> {
-    typedef uint32_t type __attribute__((ext_vector_type(1), aligned(2)));
-};
 
-// Where a lane's chunk lies in a row: V elements of the first and V of the second half of
-// the turned part (or, behind it, of the rest), so that neighbouring lanes load
-// neighbouring vectors.  Single-element chunks of an odd rest: `second` is false where the
-// row has no second element.  Places outside the row are moved to one inside.
+// Chunks of V pairs that the turned part of a row has, and the rest behind it (in vectors, two
+// to a chunk).  Pairs half the turned part apart take a vector of either half, neighbours
+// vectors of the whole part.
+template <int V>
+__host__ __device__ __forceinline__ int32_t turned_chunks(int32_t rot, bool neighbours)
+{
+    return neighbours && V > 1 ? ((rot + V - 1) / V + 1) / 2 : (rot / 2 + V - 1) / V;
+}
+template <int V>
+__host__ __device__ __forceinline__ int32_t rest_chunks(int32_t rest)
+{
+    return ((rest + V - 1) / V + 1) / 2;
+}
+
+// Where a lane's chunk lies in a row: two vectors of V elements, neighbouring lanes' side by
+// side.  The last vector of a part ends where the part ends, and so may begin before
+// the end of the one before it: its first `skip` elements are that one's.  They are worked out
+// twice, with the same result, and counted once; a rest shorter than a vector begins
+// among turned elements (`crosses`), which its lane must not store.  A chunk that the row does not
+// have is moved to its first elements.
 struct Chunk {
-    int32_t first, other;
-    bool live, second, turned;
+    int32_t first, other, skip_first, skip_other;
+    bool live, turned, crosses;
 };
 
 template <int V>
 __device__ __forceinline__ Chunk chunk_of(int32_t c, const RopeArgs &a)
 {
-    const int32_t turned = a.rot / (2 * V), rest = a.dim - a.rot;
-    Chunk k;
-    k.turned = c < turned;
-    if (V == 1 && a.interleaved && k.turned) {
-        k.first = 2 * c;
-        k.other = 2 * c + 1;
-    } else if (k.turned) {
-        k.first = V * c;
-        k.other = a.rot / 2 + V * c;
-    } else {
-        k.first = a.rot + V * (c - turned);
-        k.other = k.first + (rest + 1) / 2;
+    const int32_t rest = a.dim - a.rot, half = a.rot / 2, turned = turned_chunks<V>(a.rot, a.interleaved);
+    Chunk k = {0, 0, V, V, false, false, false};
+    // vector i of a part of n elements from `begin` on
+    const auto vector = [](int32_t i, int32_t begin, int32_t n, int32_t &at, int32_t &skip) {
+        const int32_t from = V * i < n - V ? V * i : n - V;
+        at = begin + from;
+        skip = V * i - from < V ? V * i - from : V;
+    };
+    if (c < turned) {
+        k.live = k.turned = true;
+        if (!a.interleaved) {
+            vector(c, 0, half, k.first, k.skip_first);
+            k.other = half + k.first;
+            k.skip_other = k.skip_first;
+        } else if (V == 1) {
+            k.first = 2 * c;
+            k.other = 2 * c + 1;
+            k.skip_first = k.skip_other = 0;
+        } else {
+            vector(c, 0, a.rot, k.first, k.skip_first);
+            vector(c + turned, 0, a.rot, k.other, k.skip_other);
+        }
+    } else if (c < turned + rest_chunks<V>(rest)) {
+        k.live = true;
+        k.crosses = rest < V;
+        vector(c - turned, a.rot, rest, k.first, k.skip_first);
+        vector(c - turned + rest_chunks<V>(rest), a.rot, rest, k.other, k.skip_other);
     }
-    k.live = c < turned + (rest + 2 * V - 1) / (2 * V);
-    k.second = k.live && k.other < a.dim;
-    if (!k.live)
-        k.first = 0;
-    if (!k.second)
-        k.other = k.first;
     return k;
 }
 
@@ -103,22 +126,29 @@ struct Selectors {
     }
 };
 
-// The pair in word e of chunk c.
+// The pair in word e of a turned chunk.
 template <int V>
-__device__ __forceinline__ int32_t pair_of(int32_t c, int e, const RopeArgs &a)
+__device__ __forceinline__ int32_t pair_of(const Chunk &k, int e, const RopeArgs &a)
 {
     if (V > 1 && a.interleaved)
-        return (e % 2 ? a.rot / 4 : 0) + V / 2 * c + e / 2;
-    return V * c + e;
+        return (e % 2 ? k.other : k.first) / 2 + e / 2;
+    return V == 1 && a.interleaved ? k.first / 2 : k.first + e;
 }
 
-// The column of element b (0: first, 1: second) of word e.
+// The column of element b (0: first, 1: second) of word e, and whether the chunk counts it.
 template <int V>
 __device__ __forceinline__ int32_t column_of(const Chunk &k, int e, int b, const RopeArgs &a)
 {
     if (V > 1 && a.interleaved)
         return (e % 2 ? k.other : k.first) + e / 2 * 2 + b;
     return (b ? k.other : k.first) + e;
+}
+template <int V>
+__device__ __forceinline__ bool counts(const Chunk &k, int e, int b, const RopeArgs &a)
+{
+    if (V > 1 && a.interleaved)
+        return e / 2 * 2 + b >= (e % 2 ? k.skip_other : k.skip_first);
+    return e >= (b ? k.skip_other : k.skip_first);
 }
 
 // A lane's place in the rows of one buffer: the offsets of its chunks' two vectors from the
@@ -182,17 +212,17 @@ struct Loaded<1, kChunks> {
 
     __device__ __forceinline__ void pairs(int i, const Chunk &k, const Selectors &, uint32_t (&w)[1]) const
     {
-        w[0] = p[i] | (k.second ? (uint32_t)q[i] << 16 : 0);
+        w[0] = p[i] | (k.skip_other == 0 ? (uint32_t)q[i] << 16 : 0);
     }
 };
 
-template <int V, int kChunks>
+template <bool kRagged, int V, int kChunks>
 __device__ __forceinline__ void store_pairs(uint16_t *step, const Offsets<V, kChunks> &o, int i, const Chunk &k,
                                             const Selectors &sel, const uint32_t (&w)[V])
 {
     if constexpr (V == 1) {
         *(global_ptr<uint16_t>)(step + o.first[i]) = (uint16_t)w[0];
-        if (k.second)
+        if (k.skip_other == 0)
             *(global_ptr<uint16_t>)(step + o.other[i]) = (uint16_t)(w[0] >> 16);
     } else {
         typedef typename Vec<V>::type vec;
@@ -201,6 +231,16 @@ __device__ __forceinline__ void store_pairs(uint16_t *step, const Offsets<V, kCh
         for (int j = 0; j < V / 2; ++j) {
             p[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], sel.even);
             q[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], sel.odd);
+        }
+        if (kRagged && k.crosses) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if (e >= k.skip_first)
+                    *(global_ptr<uint16_t>)(step + o.first[i] + e) = (uint16_t)(p[e / 2] >> (16 * (e % 2)));
+                if (e >= k.skip_other)
+                    *(global_ptr<uint16_t>)(step + o.other[i] + e) = (uint16_t)(q[e / 2] >> (16 * (e % 2)));
+            }
+            return;
         }
         __builtin_nontemporal_store(p, (global_ptr<vec>)(step + o.first[i]));
         __builtin_nontemporal_store(q, (global_ptr<vec>)(step + o.other[i]));
@@ -362,10 +402,9 @@ struct HeadWave {
     {
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            const int32_t c = k[i].turned ? (int32_t)(threadIdx.x & 63) % kLanes + i * 64 : 0;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float2 r = turn[pair_of<V>(c, e, a)];
+                const float2 r = turn[k[i].turned ? pair_of<V>(k[i], e, a) : 0];
                 cs[i][e] = r.x;
                 sn[i][e] = r.y;
             }
@@ -387,7 +426,7 @@ constexpr int kRopeThreads = 256;
 // the sines are worked out.
 // With the weight multiplied into the cosines and sines once for the unit, an element of a
 // step costs three operations: out_a = (x_a rstd) (w_a cos) - (x_b rstd) (w_b sin).
-template <typename T, int V, int kLanes, int kChunks, int kSteps>
+template <typename T, int V, int kLanes, int kChunks, bool kRagged, int kSteps>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a)
 {
     constexpr int kWaves = kRopeThreads / 64;
@@ -453,9 +492,15 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a)
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
                     float part_sum = 0.0f;
+                    if constexpr (kRagged) {
 #pragma unroll
-                    for (int e = 0; e < 2 * V; ++e)
-                        part_sum = __builtin_fmaf(x[i][e], x[i][e], part_sum);
+                        for (int e = 0; e < 2 * V; ++e)
+                            part_sum += counts<V>(me.k[i], e / 2, e % 2, a) ? x[i][e] * x[i][e] : 0.0f;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2 * V; ++e)
+                            part_sum = __builtin_fmaf(x[i][e], x[i][e], part_sum);
+                    }
                     sum += me.k[i].live ? part_sum : 0.0f;
                 }
                 rstd = head_rstd(lanes_sum<kLanes>(sum), a);
@@ -481,7 +526,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a)
                     }
                 }
                 if (live && me.k[i].live)
-                    store_pairs<V, kChunks>(to, out, i, me.k[i], me.sel, o);
+                    store_pairs<kRagged, V, kChunks>(to, out, i, me.k[i], me.sel, o);
             }
         }
     }
@@ -493,7 +538,7 @@ constexpr int kRopeGradThreads = 256;
 
 // Workgroups take sums: the first parts[0] the queries', the others the keys'; a wave of sum p
 // takes every parts * 4'th unit and sums the weight gradient of its lanes' chunks over them.
-template <typename T, int V, int kLanes, int kChunks>
+template <typename T, int V, int kLanes, int kChunks, bool kRagged>
 __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
 {
     constexpr int kWaves = kRopeGradThreads / 64;
@@ -564,10 +609,19 @@ __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
                     float sq = 0.0f, d = 0.0f;
+                    if constexpr (kRagged) {
 #pragma unroll
-                    for (int e = 0; e < 2 * V; ++e) {
-                        sq = __builtin_fmaf(x[i][e], x[i][e], sq);
-                        d = __builtin_fmaf(g[i][e] * x[i][e], me.w[i][e], d);
+                        for (int e = 0; e < 2 * V; ++e) {
+                            const bool own = counts<V>(me.k[i], e / 2, e % 2, a);
+                            sq += own ? x[i][e] * x[i][e] : 0.0f;
+                            d += own ? g[i][e] * x[i][e] * me.w[i][e] : 0.0f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2 * V; ++e) {
+                            sq = __builtin_fmaf(x[i][e], x[i][e], sq);
+                            d = __builtin_fmaf(g[i][e] * x[i][e], me.w[i][e], d);
+                        }
                     }
                     squares += me.k[i].live ? sq : 0.0f;
                     dot += me.k[i].live ? d : 0.0f;
@@ -594,7 +648,7 @@ __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
                 for (int e = 0; e < V; ++e)
                     o[e] = T::pack(g[i][2 * e], g[i][2 * e + 1]);
                 if (live && me.k[i].live)
-                    store_pairs<V, kChunks>(to, out, i, me.k[i], me.sel, o);
+                    store_pairs<kRagged, V, kChunks>(to, out, i, me.k[i], me.sel, o);
             }
             p = ahead;
         }
@@ -608,7 +662,7 @@ __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
 #pragma unroll
                 for (int m = kLanes; m < 64; m *= 2)
                     acc[i][e] += __shfl_xor(acc[i][e], m, 64);
-                if (lane < kLanes && me.k[i].live && (V > 1 || e == 0 || me.k[i].second))
+                if (lane < kLanes && me.k[i].live && ((V > 1 && !kRagged) || counts<V>(me.k[i], e / 2, e % 2, a)))
                     sums[wave][column_of<V>(me.k[i], e / 2, e % 2, a)] = acc[i][e];
             }
         __syncthreads();
@@ -785,7 +839,7 @@ void fill_args(RopeArgs *a, int64_t tokens, int64_t head_dim, double eps, const 
 
 constexpr int64_t kFewSteps = 2048;
 
-template <typename T, int V, int kLanes, int kChunks, int kSteps>
+template <typename T, int V, int kLanes, int kChunks, bool kRagged, int kSteps>
 zr_status rope_steps(RopeArgs *a, hipStream_t st)
 {
     constexpr int kHeads = 64 / kLanes, kWaves = kRopeThreads / 64;
@@ -795,91 +849,119 @@ zr_status rope_steps(RopeArgs *a, hipStream_t st)
         a->parts[t] = (int32_t)((steps + a->per[t] - 1) / a->per[t]);
     }
     const int64_t blocks = (a->tokens + kWaves - 1) / kWaves * (a->parts[0] + a->parts[1]);
-    return launch(rope_kernel<T, V, kLanes, kChunks, kSteps>, grid_of(blocks), dim3(kRopeThreads), 0, st, *a);
+    return launch(rope_kernel<T, V, kLanes, kChunks, kRagged, kSteps>, grid_of(blocks), dim3(kRopeThreads), 0, st, *a);
 }
 
 // Few tokens: a wave to a step, for latency.  Else a unit is a token's steps, four at most.
-template <typename T, int V, int kLanes, int kChunks>
+template <typename T, int V, int kLanes, int kChunks, bool kRagged>
 zr_status rope_launch(RopeArgs *a, hipStream_t st)
 {
     constexpr int kHeads = 64 / kLanes;
     const int64_t steps = (a->t[0].heads + kHeads - 1) / kHeads + (a->t[1].heads + kHeads - 1) / kHeads;
-    return a->tokens * steps <= kFewSteps ? rope_steps<T, V, kLanes, kChunks, 1>(a, st)
-                                          : rope_steps<T, V, kLanes, kChunks, 4>(a, st);
+    return a->tokens * steps <= kFewSteps ? rope_steps<T, V, kLanes, kChunks, kRagged, 1>(a, st)
+                                          : rope_steps<T, V, kLanes, kChunks, kRagged, 4>(a, st);
 }
 
 // Steps of a unit, at most: its waves take the sines once for them, and all waves end within
 // a unit of one another.
 constexpr int64_t kUnitSteps = 2;
 
-// Parts go to the tensors by their heads; units are smaller where they would be too few to
-// give every wave one.
-template <typename T, int V, int kLanes, int kChunks>
+// Sums go to the tensors by their work, a unit's sines counted as half a step; units are
+// smaller where they would be too few to give every wave one.
+template <typename T, int V, int kLanes, int kChunks, bool kRagged>
 zr_status rope_grad_launch(RopeArgs *a, hipStream_t st)
 {
     constexpr int kHeads = 64 / kLanes, kWaves = kRopeGradThreads / 64;
     const int64_t heads = (int64_t)a->t[0].heads + a->t[1].heads;
+    int64_t units[2] = {0, 0};
+    double work[2] = {0.0, 0.0};
     for (int t = 0; t < 2; ++t)
         if (a->t[t].heads > 0) {
-            int64_t share = kGradParts * a->t[t].heads / heads;
-            share = share < 1 ? 1 : share > kGradParts - 1 && a->t[1 - t].heads > 0 ? kGradParts - 1 : share;
-            const int64_t steps = (a->t[t].heads + kHeads - 1) / kHeads, waves = share * kWaves;
-            int64_t splits = (waves + a->tokens - 1) / a->tokens;
-            splits = splits > (steps + kUnitSteps - 1) / kUnitSteps ? splits : (steps + kUnitSteps - 1) / kUnitSteps;
-            splits = splits < steps ? splits : steps;
+            const int64_t steps = (a->t[t].heads + kHeads - 1) / kHeads;
+            const int64_t waves = kGradParts * kWaves * a->t[t].heads / heads + 1;
+            int64_t splits = std::max((waves + a->tokens - 1) / a->tokens, (steps + kUnitSteps - 1) / kUnitSteps);
+            splits = std::min(splits, steps);
             a->per[t] = (int32_t)((steps + splits - 1) / splits);
-            const int64_t units = a->tokens * ((steps + a->per[t] - 1) / a->per[t]), most = (units + kWaves - 1) / kWaves;
-            a->parts[t] = (int32_t)(share < most ? share : most);
+            units[t] = a->tokens * ((steps + a->per[t] - 1) / a->per[t]);
+            work[t] = (double)units[t] * (a->per[t] + 0.5);
         }
-    return launch(rope_grad_kernel<T, V, kLanes, kChunks>, grid_of(a->parts[0] + a->parts[1]), dim3(kRopeGradThreads), 0,
-                  st, *a);
+    const int64_t queries = std::min<int64_t>(std::max<int64_t>((int64_t)(kGradParts * work[0] / (work[0] + work[1]) + 0.5), 1),
+                                              kGradParts - 1);
+    for (int t = 0; t < 2; ++t) {
+        const int64_t share = units[1 - t] == 0 ? kGradParts : t == 0 ? queries : kGradParts - queries;
+        a->parts[t] = (int32_t)std::min(share, (units[t] + kWaves - 1) / kWaves);
+    }
+    return launch(rope_grad_kernel<T, V, kLanes, kChunks, kRagged>, grid_of(a->parts[0] + a->parts[1]),
+                  dim3(kRopeGradThreads), 0, st, *a);
 }
 
-// The layout of a row: vectors of 8 or 4 (2) elements where both halves of the turned part
-// and of the rest are whole vectors, else single elements; as many lanes as its chunks need.
-// Forward, vectors of 4 leave room for 7 waves to a SIMD where those of 8 leave 4 (5003
-// tokens of 24 heads of 96: 12.4 us and 14.9; 16384 of 40 of 128: 57.7 and 57.3); backward,
-// where sums stay in registers anyway, 8 need half as many steps (118 us and 99).
-template <typename T, bool kForward, int V, int kLanes, int kChunks>
+// Lanes for the chunks of a row, the least of 4 ... 64 (0: more than a wave has); 0 also where a
+// vector is longer than what it has to lie in.
+template <int V>
+int32_t lanes_of(const RopeArgs &a)
+{
+    if (a.dim < V || (a.rot > 0 && (a.interleaved ? a.rot : a.rot / 2) < V))
+        return 0;
+    const int32_t chunks = turned_chunks<V>(a.rot, a.interleaved) + rest_chunks<V>(a.dim - a.rot);
+    for (int32_t lanes = 4; lanes <= 64; lanes *= 2)
+        if (chunks <= lanes)
+            return lanes;
+    return 0;
+}
+
+// Whether the last vector of a part begins before the end of the one before it.
+template <int V>
+bool ragged(const RopeArgs &a)
+{
+    return (a.interleaved ? a.rot % (2 * V) : a.rot / 2 % V) != 0 || (a.dim - a.rot) % (2 * V) != 0;
+}
+
+template <typename T, bool kForward, int V, int kLanes, int kChunks, bool kRagged>
 zr_status layout_launch(RopeArgs *a, hipStream_t st)
 {
     if constexpr (kForward)
-        return rope_launch<T, V, kLanes, kChunks>(a, st);
+        return rope_launch<T, V, kLanes, kChunks, kRagged>(a, st);
     else
-        return rope_grad_launch<T, V, kLanes, kChunks>(a, st);
+        return rope_grad_launch<T, V, kLanes, kChunks, kRagged>(a, st);
 }
 
+template <typename T, bool kForward, int V, bool kRagged>
+zr_status vector_launch(RopeArgs *a, int32_t lanes, hipStream_t st)
+{
+    switch (lanes) {
+    case 4: return layout_launch<T, kForward, V, 4, 1, kRagged>(a, st);
+    case 8: return layout_launch<T, kForward, V, 8, 1, kRagged>(a, st);
+    case 16: return layout_launch<T, kForward, V, 16, 1, kRagged>(a, st);
+    case 32: return layout_launch<T, kForward, V, 32, 1, kRagged>(a, st);
+    default: break;
+    }
+    // 32 chunks of 8 pairs are the longest row: only a ragged one has 33
+    constexpr int kMost = V == 8 && !kRagged ? 32 : 64;
+    return layout_launch<T, kForward, V, kMost, 1, kRagged>(a, st);
+}
+
+// Forward, vectors of 4 elements leave room for 7 waves to a SIMD where those of 8 leave 4
+// (5003 tokens of 24 heads of 96: 12.4 us and 14.9; 16384 of 40 of 128: 57.7 and 57.3).
+// Backward, where sums stay in registers anyway, 8 take half as many steps (99 us and 118).
+// What those do not fit (65 chunks forward; parts shorter than a vector) takes the other
+// kind, heads too short for both single elements.
 template <typename T, bool kForward>
 zr_status for_layout(RopeArgs *a, hipStream_t st)
 {
-    const int32_t rest = a->dim - a->rot;
-    if constexpr (!kForward)
-        if (a->rot % 16 == 0 && rest % 16 == 0) {
-            if (a->dim <= 64)
-                return layout_launch<T, kForward, 8, 4, 1>(a, st);
-            if (a->dim <= 128)
-                return layout_launch<T, kForward, 8, 8, 1>(a, st);
-            if (a->dim <= 256)
-                return layout_launch<T, kForward, 8, 16, 1>(a, st);
-            return layout_launch<T, kForward, 8, 32, 1>(a, st);
-        }
-    if (a->rot % 8 == 0 && rest % 8 == 0) {
-        if (a->dim <= 64)
-            return layout_launch<T, kForward, 4, 8, 1>(a, st);
-        if (a->dim <= 128)
-            return layout_launch<T, kForward, 4, 16, 1>(a, st);
-        if (a->dim <= 256)
-            return layout_launch<T, kForward, 4, 32, 1>(a, st);
-        return layout_launch<T, kForward, 4, 64, 1>(a, st);
-    }
-    if (a->rot % 4 == 0 && rest % 4 == 0) {
-        if (a->dim <= 128)
-            return layout_launch<T, kForward, 2, 32, 1>(a, st);
-        return layout_launch<T, kForward, 2, 64, 2>(a, st);
+    constexpr int kFirst = kForward ? 4 : 8;
+    if (const int32_t lanes = lanes_of<kFirst>(*a))
+        return ragged<kFirst>(*a) ? vector_launch<T, kForward, kFirst, true>(a, lanes, st)
+                                  : vector_launch<T, kForward, kFirst, false>(a, lanes, st);
+    if constexpr (kForward) {
+        if (lanes_of<8>(*a))
+            return layout_launch<T, kForward, 8, 64, 1, true>(a, st);
+    } else {
+        if (const int32_t lanes = lanes_of<4>(*a))
+            return vector_launch<T, kForward, 4, true>(a, lanes, st);
     }
     if (a->dim <= 128)
-        return layout_launch<T, kForward, 1, 64, 1>(a, st);
-    return layout_launch<T, kForward, 1, 64, 4>(a, st);
+        return layout_launch<T, kForward, 1, 64, 1, false>(a, st);
+    return layout_launch<T, kForward, 1, 64, 4, false>(a, st);
 }
 
 int64_t heads_of(const zr_heads *h) { return h ? h->heads : 0; }
