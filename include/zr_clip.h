@@ -63,7 +63,7 @@ typedef struct zr_clip_hparams {
  * every rank, once the sum has been all-reduced.
  *
  * grads: host array of n device pointers (n >= 0; an entry may be NULL where numels is
- * 0); numels: host array of n element counts (>= 0).  dtype: ZR_BF16, ZR_F16 or ZR_F32.
+ * 0); numels: host array of n element counts (0 ... 2^42).  dtype: ZR_BF16, ZR_F16 or ZR_F32.
  * hp: host pointer.  ls may be NULL.  workspace: device fp64 [ZR_GRAD_NORM_PARTIALS],
  * contents undefined before and after; two calls that may run at once need workspaces and
  * records of their own, and so do two graphs whose replays may.  The tensors may overlap
@@ -86,8 +86,9 @@ ZR_API zr_status zr_clip_grads(void *const *grads, const int64_t *numels, int32_
 /*
  * zr_adamw_step on the gradient multiplied by clip->factor: its update with grad_scale *
  * factor (one fp64 product) in the place of grad_scale, bit for bit.  The clipped
- * gradient is not written: clipping costs the step no pass over memory.  The graph calls
- * of zr.h treat it as a call of the AdamW family.  Buffer rules as zr_adamw_step; the
+ * gradient is not written: clipping costs the step no pass over memory.  A factor of NaN
+ * makes every state NaN, as a gradient of NaN does; only the fp16 form skips such a step.
+ * The graph calls of zr.h treat it as a call of the AdamW family.  Buffer rules as zr_adamw_step; the
  * record must not overlap a buffer.  Errors: ZR_EINVAL, ZR_EALIGN, ZR_EHIP.
  */
 ZR_API zr_status zr_adamw_step_clip(const void *grad, float *master, float *exp_avg, float *exp_avg_sq,

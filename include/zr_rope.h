@@ -19,7 +19,7 @@
  * The angle is an fp64 product, reduced to one turn in fp64 before its sine and cosine
  * are taken in fp32: positions of 2^31 at a frequency of 1 still have angles right to 2^-20.
  * All other arithmetic is fp32, each output rounded once; a row whose squares pass fp32's
- * range (magnitudes from about 1e19 on) has rstd 0.
+ * range (magnitudes from about 1e19 on) has rstd 0, and outputs and gradients 0 with it.
  *
  * The conventions of zr.h hold for every call: validation first, nothing launched and
  * nothing written on an error, asynchronous on `stream`, no device allocation,
@@ -69,8 +69,8 @@ typedef struct zr_rope {
  * exactly k.  Otherwise no output may overlap another buffer; heads of one fused row
  * (equal token strides, ranges of the row that do not meet) do not count as overlapping.
  * positions: device int64 [axes][position_stride] with position_stride >= tokens where
- * axes > 1, any values.  tokens >= 0 (0 is a no-op), 1 <= head_dim <= ZR_MAX_HEAD_DIM, eps
- * finite and >= 0.  positions may be NULL where rot_dim is 0.
+ * axes > 1, any values.  0 <= tokens <= 2^48 (0 is a no-op), heads <= 65536, 1 <= head_dim <=
+ * ZR_MAX_HEAD_DIM, eps finite and >= 0.  positions may be NULL where rot_dim is 0.
  * Errors: ZR_EINVAL, ZR_EALIGN, ZR_EHIP.
  */
 ZR_API zr_status zr_qk_norm_rope(const zr_heads *q, const zr_heads *k, const void *q_weight, const void *k_weight,

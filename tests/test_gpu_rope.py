@@ -316,6 +316,39 @@ def test_infinities_stay_in_their_row():
     assert not out.any()
 
 
+@pytest.mark.parametrize("d,rot", [(128, 128), (66, 66), (33, 18)])
+def test_rows_past_the_range_of_their_squares(d, rot):
+    """Magnitudes of 1e20 and more: rstd 0, and with it the outputs and every gradient; the other
+    rows are as without them."""
+    device()
+    c = case(12, 6, 2, d, rot, BF)
+    clean = check_forward(c)
+    at = [(1, 0), (7, 5), (11, 3)]
+    dy = [torch.randn(x.shape, device="cuda").to(BF) for x in clean]
+    run = lambda: backward_of(c, dy)  # noqa: E731
+    for token, head in at:
+        c["q"][token, head] = 0.0
+    dq0, _, dwq0, _ = run()
+    for i, (token, head) in enumerate(at):
+        c["q"][token, head] = torch.tensor([1e20, -1e30, 3e38][i], device="cuda").to(BF)
+    q, k = torch.empty_like(clean[0]), torch.empty_like(clean[1])
+    zr.zr_qk_norm_rope(c["q"], c["k"], c["wq"], c["wk"], c["positions"], c["rope"], q, k)
+    dq, _, dwq, _ = run()
+    keep = torch.ones(12, 6, dtype=torch.bool, device="cuda")
+    for token, head in at:
+        keep[token, head] = False
+    assert not q[~keep].any() and torch.equal(q[keep], clean[0][keep])
+    assert not dq[~keep].any() and torch.equal(dq[keep], dq0[keep])
+    assert torch.equal(dwq, dwq0)
+
+
+def backward_of(c, dy, eps=1e-5):
+    d = c["q"].shape[2]
+    out = [torch.empty_like(x) for x in dy] + [torch.empty(d, dtype=BF, device="cuda") for _ in "qk"]
+    zr.zr_qk_norm_rope_backward(*dy, c["q"], c["k"], c["wq"], c["wk"], c["positions"], c["rope"], *out, zr.qk_norm_workspace(d), eps=eps)
+    return out
+
+
 @pytest.mark.parametrize("d,rot", [(128, 128), (72, 72), (33, 18)])
 def test_same_bits_on_any_grid(d, rot, monkeypatch):
     device()

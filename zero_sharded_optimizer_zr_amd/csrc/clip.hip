@@ -417,6 +417,8 @@ zr_status check_clip(const char *who, const void *clip)
     return ZR_OK;
 }
 
+constexpr int64_t kMostBytes = (int64_t)1 << 44;  // 2^31 tiles
+
 // Checks a tensor list; buffers p[i] of b[i] bytes (NULL: none) must not overlap a tensor.
 zr_status check_list(const char *who, const void *const *grads, const int64_t *numels, int32_t n, zr_dtype dtype,
                      const void *const *p, const int64_t *b, int count)
@@ -429,7 +431,7 @@ zr_status check_list(const char *who, const void *const *grads, const int64_t *n
     for (int32_t t = 0; t < n; ++t) {
         if (numels[t] < 0 || (numels[t] > 0 && !grads[t]))
             return fail(ZR_EINVAL, "%s: numels[%d] < 0 or grads[%d] is NULL", who, t, t);
-        if (numels[t] > (int64_t)1 << 42)  // 2^31 tiles of fp32; no device holds as much
+        if (numels[t] > kMostBytes / 4)  // no device holds as much
             return fail(ZR_EINVAL, "%s: numels[%d] past 2^42", who, t);
         if (!aligned_to(grads[t], size))
             return fail(ZR_EALIGN, "%s: grads[%d] must be %d-byte aligned", who, t, (int)size);
@@ -466,7 +468,9 @@ zr_status for_batches(const void *const *grads, const int64_t *numels, int32_t n
         const uintptr_t p = reinterpret_cast<uintptr_t>(grads[t]);
         int64_t bytes = size * numels[t++];
         if constexpr (kInPlace) {
-            for (; t < n && (numels[t] == 0 || reinterpret_cast<uintptr_t>(grads[t]) == p + (uintptr_t)bytes); ++t)
+            for (; t < n && bytes < kMostBytes &&
+                   (numels[t] == 0 || reinterpret_cast<uintptr_t>(grads[t]) == p + (uintptr_t)bytes);
+                 ++t)
                 bytes += size * numels[t];
             bytes += (int64_t)(p & 127);
         }

@@ -5,11 +5,11 @@
 // angle = position * inv_freq.  Backward: the gradient turned back, then the norm's:
 // dw = sum g xh, dx = rstd * (g w - xh * mean(g w xh)).
 //
-// A head's row lies in a group of kGroupLanes lanes, a lane holding a chunk of V pairs
+// A head's row lies in a group of kLanes lanes, a lane holding a chunk of V pairs
 // (2V elements) as V words, a pair to a word: both elements of a pair are in one lane,
 // and turning takes no exchange.  Where the pairs are halves of the row apart, a lane
 // loads V elements of either half and the words are put together by byte permutes; where
-// they are neighbours the loaded words are the pairs.  A wave works on 64 / kGroupLanes
+// they are neighbours the loaded words are the pairs.  A wave works on 64 / kLanes
 // heads of one token at a time, so that a token's sines and cosines, taken once by the
 // wave (a lane to a pair) and handed over through LDS, serve all its heads.
 #include <algorithm>
@@ -247,6 +247,19 @@ __device__ __forceinline__ void store_pairs(uint16_t *step, const Offsets<V, kCh
     }
 }
 
+// Sum of u * v over the elements of a chunk that it counts; 0 for a chunk that is not there.
+template <int V, bool kRagged>
+__device__ __forceinline__ float dot_of(const Chunk &k, const RopeArgs &a, const float (&u)[2 * V], const float (&v)[2 * V])
+{
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e) {
+        const float next = __builtin_fmaf(u[e], v[e], sum);
+        sum = !kRagged || counts<V>(k, e / 2, e % 2, a) ? next : sum;
+    }
+    return k.live ? sum : 0.0f;
+}
+
 // Sum over each group of kLanes lanes, the same bits in all of them.
 template <int kLanes>
 __device__ __forceinline__ float lanes_sum(float a)
@@ -333,8 +346,8 @@ __device__ __forceinline__ float head_rstd(float squares, const RopeArgs &a)
 template <int V, int kLanes, int kChunks>
 constexpr int kPairsOf = (V * kLanes * kChunks + 63) / 64;
 
-// What the waves of both passes share.  A step is 64 / kLanes heads of a token, a unit `per`
-// steps of one token; a wave takes every stride'th unit of one tensor.
+// What the waves of both passes share: one tensor's rows.  A step is 64 / kLanes heads of a
+// token, a unit `per` steps of one token; backward, a wave takes every stride'th unit.
 template <typename T, int V, int kLanes, int kChunks>
 struct HeadWave {
     static constexpr int kHeads = 64 / kLanes;
@@ -490,19 +503,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a)
             if (t.w) {
                 float sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    float part_sum = 0.0f;
-                    if constexpr (kRagged) {
-#pragma unroll
-                        for (int e = 0; e < 2 * V; ++e)
-                            part_sum += counts<V>(me.k[i], e / 2, e % 2, a) ? x[i][e] * x[i][e] : 0.0f;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 2 * V; ++e)
-                            part_sum = __builtin_fmaf(x[i][e], x[i][e], part_sum);
-                    }
-                    sum += me.k[i].live ? part_sum : 0.0f;
-                }
+                for (int i = 0; i < kChunks; ++i)
+                    sum += dot_of<V, kRagged>(me.k[i], a, x[i], x[i]);
                 rstd = head_rstd(lanes_sum<kLanes>(sum), a);
             }
             uint16_t *to = t.out + me.at(p, t.out_token, t.out_head);
@@ -605,40 +607,36 @@ __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
                 ask(ahead);
             const bool live = me.has_head(p);
             if (t.w) {
-                float squares = 0.0f, dot = 0.0f;
+                float squares = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    float sq = 0.0f, d = 0.0f;
-                    if constexpr (kRagged) {
-#pragma unroll
-                        for (int e = 0; e < 2 * V; ++e) {
-                            const bool own = counts<V>(me.k[i], e / 2, e % 2, a);
-                            sq += own ? x[i][e] * x[i][e] : 0.0f;
-                            d += own ? g[i][e] * x[i][e] * me.w[i][e] : 0.0f;
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 2 * V; ++e) {
-                            sq = __builtin_fmaf(x[i][e], x[i][e], sq);
-                            d = __builtin_fmaf(g[i][e] * x[i][e], me.w[i][e], d);
-                        }
-                    }
-                    squares += me.k[i].live ? sq : 0.0f;
-                    dot += me.k[i].live ? d : 0.0f;
-                }
-                squares = lanes_sum<kLanes>(squares);
-                dot = lanes_sum<kLanes>(dot);
-                const float rstd = head_rstd(squares, a), along = dot * a.inv_dim * rstd * rstd;
-                // a head that is not there stands for the step's first: it adds nothing, and no
-                // NaN that the first does not add
-                const float counted = live ? rstd : 0.0f;
+                for (int i = 0; i < kChunks; ++i)
+                    squares += dot_of<V, kRagged>(me.k[i], a, x[i], x[i]);
+                const float rstd = head_rstd(lanes_sum<kLanes>(squares), a);
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-                    for (int e = 0; e < 2 * V; ++e) {
-                        acc[i][e] = __builtin_fmaf(g[i][e] * x[i][e], counted, acc[i][e]);
-                        g[i][e] = __builtin_fmaf(-along, x[i][e], g[i][e] * me.w[i][e]) * rstd;
-                    }
+                    for (int e = 0; e < 2 * V; ++e)
+                        x[i][e] *= rstd;
+                if (live)  // one that is not there stands for the step's first head
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2 * V; ++e)
+                            acc[i][e] = __builtin_fmaf(g[i][e], x[i][e], acc[i][e]);
+                float dot = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+#pragma unroll
+                    for (int e = 0; e < 2 * V; ++e)
+                        g[i][e] *= me.w[i][e];
+                    dot += dot_of<V, kRagged>(me.k[i], a, g[i], x[i]);
+                }
+                const float along = lanes_sum<kLanes>(dot) * a.inv_dim;
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2 * V; ++e)
+                        g[i][e] = __builtin_fmaf(-along, x[i][e], g[i][e]) * rstd;
             }
             uint16_t *to = t.out + me.at(p, t.out_token, t.out_head);
 #pragma unroll
@@ -677,14 +675,14 @@ __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
     }
 }
 
-// Weight gradients from the partial sums: a workgroup takes 32 columns of one tensor, 16
-// threads to a column, each every 16th partial sum; they meet in LDS in that order.
 // Partial sums that a call makes, at most: two workgroups to a compute unit.
 constexpr int64_t kGradParts = 512;
 static_assert(kGradParts <= ZR_QK_PARTIALS, "the workspace holds them");
 
 constexpr int kDweightThreads = 512;
 
+// Weight gradients from the partial sums: a workgroup takes 32 columns of one tensor, 16
+// threads to a column, each every 16th partial sum; they meet in LDS in that order.
 template <typename T>
 __global__ __launch_bounds__(kDweightThreads) void rope_dweight_kernel(const float *partial, int32_t dim, int32_t q_parts,
                                                                         int32_t k_parts, uint16_t *dq, uint16_t *dk)
@@ -785,8 +783,8 @@ zr_status check_rope(const char *who, zr_dtype dtype, int64_t tokens, int64_t he
 {
     if (dtype != ZR_BF16 && dtype != ZR_F16)
         return fail(ZR_EINVAL, "%s: dtype = %d, must be ZR_BF16 or ZR_F16", who, dtype);
-    if (tokens < 0 || head_dim < 1 || head_dim > ZR_MAX_HEAD_DIM)
-        return fail(ZR_EINVAL, "%s: tokens < 0 or head_dim outside [1, %d]", who, ZR_MAX_HEAD_DIM);
+    if (tokens < 0 || tokens > (int64_t)1 << 48 || head_dim < 1 || head_dim > ZR_MAX_HEAD_DIM)
+        return fail(ZR_EINVAL, "%s: tokens outside [0, 2^48] or head_dim outside [1, %d]", who, ZR_MAX_HEAD_DIM);
     if (!(eps >= 0.0) || !std::isfinite(eps) || !std::isfinite((float)eps))
         return fail(ZR_EINVAL, "%s: eps must be finite and >= 0", who);
     if ((q && (q->heads < 0 || q->heads > 65536)) || (k && (k->heads < 0 || k->heads > 65536)))
