@@ -183,9 +183,10 @@ DIMS = [(128, 128), (128, 64), (128, 32), (64, 64), (96, 96), (80, 80), (80, 20)
 @pytest.mark.parametrize("d,rot", DIMS)
 def test_head_sizes(d, rot, interleaved, dtype):
     device()
-    c = case(13, 5, 3, d, rot, dtype, interleaved, seed=d + rot)
-    check_forward(c)
-    check_backward(c)
+    for t in (13, 2100):  # few steps and many (over 4096) have kernels of their own
+        c = case(t, 5, 3, d, rot, dtype, interleaved, seed=d + rot)
+        check_forward(c)
+        check_backward(c)
 
 
 @pytest.mark.parametrize("layout", ["heads", "row", "before"])
@@ -352,7 +353,7 @@ def backward_of(c, dy, eps=1e-5):
 @pytest.mark.parametrize("d,rot", [(128, 128), (72, 72), (33, 18)])
 def test_same_bits_on_any_grid(d, rot, monkeypatch):
     device()
-    for t in (40, 300):
+    for t in (40, 300, 3000):
         c = case(t, 12, 4, d, rot, BF)
         one = check_forward(c) + check_backward(c)
         for cap in ("8", "24"):

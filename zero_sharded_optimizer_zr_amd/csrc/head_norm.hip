@@ -867,35 +867,54 @@ zr_status rope_launch(RopeArgs *a, hipStream_t st)
                                           : rope_steps<T, V, kLanes, kChunks, kRagged, 4>(a, st);
 }
 
-// Steps of a unit, at most: its waves take the sines once for them, and all waves end within
-// a unit of one another.
-constexpr int64_t kUnitSteps = 2;
+// Divides a backward pass among kGradParts workgroups of `waves` waves: per and parts of each
+// tensor, for `steps` steps a token.  A unit costs its steps and half of one for its sines;
+// every wave of a tensor takes the same number of units, and the most that any wave takes
+// is as little as the workgroups allow (units of two steps where one does not give less).
+void divide_backward(RopeArgs *a, const int64_t (&steps)[2], int64_t waves)
+{
+    int64_t best = 0;
+    for (int32_t pair = 3; pair >= 0; --pair) {
+        const int64_t per[2] = {1 + (pair & 1), 1 + (pair >> 1)};
+        if ((per[0] > 1 && per[0] > steps[0]) || (per[1] > 1 && per[1] > steps[1]))
+            continue;
+        int64_t units[2], parts[2];
+        for (int t = 0; t < 2; ++t)
+            units[t] = a->tokens * ((steps[t] + per[t] - 1) / per[t]);
+        // workgroups that waves with work for `most` half steps need
+        const auto needed = [&](int64_t most) {
+            for (int t = 0; t < 2; ++t) {
+                const int64_t each = waves * (most / (2 * per[t] + 1));  // units of a workgroup
+                parts[t] = units[t] == 0 ? 0 : each == 0 ? kGradParts + 1 : (units[t] + each - 1) / each;
+            }
+            return parts[0] + parts[1];
+        };
+        int64_t low = 1, high = 8;
+        while (needed(high) > kGradParts)
+            high *= 2;
+        while (low < high) {
+            const int64_t middle = low + (high - low) / 2;
+            if (needed(middle) > kGradParts)
+                low = middle + 1;
+            else
+                high = middle;
+        }
+        if (best == 0 || low < best) {
+            best = low;
+            needed(low);
+            for (int t = 0; t < 2; ++t) {
+                a->per[t] = (int32_t)per[t];
+                a->parts[t] = (int32_t)parts[t];
+            }
+        }
+    }
+}
 
-// Sums go to the tensors by their work, a unit's sines counted as half a step; units are
-// smaller where they would be too few to give every wave one.
 template <typename T, int V, int kLanes, int kChunks, bool kRagged>
 zr_status rope_grad_launch(RopeArgs *a, hipStream_t st)
 {
-    constexpr int kHeads = 64 / kLanes, kWaves = kRopeGradThreads / 64;
-    const int64_t heads = (int64_t)a->t[0].heads + a->t[1].heads;
-    int64_t units[2] = {0, 0};
-    double work[2] = {0.0, 0.0};
-    for (int t = 0; t < 2; ++t)
-        if (a->t[t].heads > 0) {
-            const int64_t steps = (a->t[t].heads + kHeads - 1) / kHeads;
-            const int64_t waves = kGradParts * kWaves * a->t[t].heads / heads + 1;
-            int64_t splits = std::max((waves + a->tokens - 1) / a->tokens, (steps + kUnitSteps - 1) / kUnitSteps);
-            splits = std::min(splits, steps);
-            a->per[t] = (int32_t)((steps + splits - 1) / splits);
-            units[t] = a->tokens * ((steps + a->per[t] - 1) / a->per[t]);
-            work[t] = (double)units[t] * (a->per[t] + 0.5);
-        }
-    const int64_t queries = std::min<int64_t>(std::max<int64_t>((int64_t)(kGradParts * work[0] / (work[0] + work[1]) + 0.5), 1),
-                                              kGradParts - 1);
-    for (int t = 0; t < 2; ++t) {
-        const int64_t share = units[1 - t] == 0 ? kGradParts : t == 0 ? queries : kGradParts - queries;
-        a->parts[t] = (int32_t)std::min(share, (units[t] + kWaves - 1) / kWaves);
-    }
+    constexpr int kHeads = 64 / kLanes;
+    divide_backward(a, {(a->t[0].heads + kHeads - 1) / kHeads, (a->t[1].heads + kHeads - 1) / kHeads}, kRopeGradThreads / 64);
     return launch(rope_grad_kernel<T, V, kLanes, kChunks, kRagged>, grid_of(a->parts[0] + a->parts[1]),
                   dim3(kRopeGradThreads), 0, st, *a);
 }
@@ -945,24 +964,32 @@ zr_status vector_launch(RopeArgs *a, int32_t lanes, hipStream_t st)
     return layout_launch<T, kForward, V, kMost, 1, kRagged>(a, st);
 }
 
+constexpr int64_t kFewBackward = 4096;
+
 // Forward, vectors of 4 elements leave room for 7 waves to a SIMD where those of 8 leave 4
 // (5003 tokens of 24 heads of 96: 12.4 us and 14.9; 16384 of 40 of 128: 57.7 and 57.3).
-// Backward, where sums stay in registers anyway, 8 take half as many steps (99 us and 118).
+// Backward, where sums stay in registers anyway, 8 take half as many steps (99 us and 118), but
+// where those are few, what counts is how long one takes, and the sums behind it (64 tokens of
+// 40 heads of 128 in a replayed graph 8.2 us and 6.4, 777 11.1 and 11.2, 2048 19.5 and 22.0).
 // What those do not fit (65 chunks forward; parts shorter than a vector) takes the other
 // kind, heads too short for both single elements.
 template <typename T, bool kForward>
 zr_status for_layout(RopeArgs *a, hipStream_t st)
 {
-    constexpr int kFirst = kForward ? 4 : 8;
-    if (const int32_t lanes = lanes_of<kFirst>(*a))
-        return ragged<kFirst>(*a) ? vector_launch<T, kForward, kFirst, true>(a, lanes, st)
-                                  : vector_launch<T, kForward, kFirst, false>(a, lanes, st);
+    const int32_t four = lanes_of<4>(*a), eight = lanes_of<8>(*a);
     if constexpr (kForward) {
-        if (lanes_of<8>(*a))
-            return layout_launch<T, kForward, 8, 64, 1, true>(a, st);
+        if (four)
+            return ragged<4>(*a) ? vector_launch<T, true, 4, true>(a, four, st) : vector_launch<T, true, 4, false>(a, four, st);
+        if (eight)
+            return layout_launch<T, true, 8, 64, 1, true>(a, st);
     } else {
-        if (const int32_t lanes = lanes_of<4>(*a))
-            return vector_launch<T, kForward, 4, true>(a, lanes, st);
+        // steps of 64 / lanes heads
+        const bool few = eight && a->tokens <= kFewBackward &&
+                         a->tokens * ((a->t[0].heads * eight + 63) / 64 + (a->t[1].heads * eight + 63) / 64) <= kFewBackward;
+        if (eight && !(few && four))
+            return ragged<8>(*a) ? vector_launch<T, false, 8, true>(a, eight, st) : vector_launch<T, false, 8, false>(a, eight, st);
+        if (four)
+            return vector_launch<T, false, 4, true>(a, four, st);
     }
     if (a->dim <= 128)
         return layout_launch<T, kForward, 1, 64, 1, false>(a, st);
