@@ -317,6 +317,31 @@ def test_infinities_stay_in_their_row():
     assert not out.any()
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-31, 1e-6, 3.0])
+def test_eps(eps):
+    """Both ways of the reciprocal root.  Values of 1e-12 (squares of 1e-24) and of 1: the
+    first are all eps at 1e-6, and none of it at 1e-31."""
+    device()
+    for d, rot in ((128, 128), (33, 18)):
+        c = case(40, 5, 3, d, rot, BF)
+        c["q"][::2] *= 1e-12
+        check_forward(c, eps=eps)
+        check_backward(c, eps=eps)
+
+
+def test_rows_of_zeros_without_eps():
+    """0 / 0 in their own rows alone; their gradient is NaN, as the formula's."""
+    device()
+    c = case(9, 5, 3, 128, 128, BF)
+    clean = check_forward(c, eps=0.0)
+    c["q"][4, 2] = 0.0
+    q, k = torch.empty_like(clean[0]), torch.empty_like(clean[1])
+    zr.zr_qk_norm_rope(c["q"], c["k"], c["wq"], c["wk"], c["positions"], c["rope"], q, k, eps=0.0)
+    rest = torch.ones(9, 5, dtype=torch.bool, device="cuda")
+    rest[4, 2] = False
+    assert bool(q[4, 2].isnan().all()) and torch.equal(q[rest], clean[0][rest]) and torch.equal(k, clean[1])
+
+
 @pytest.mark.parametrize("d,rot", [(128, 128), (66, 66), (33, 18)])
 def test_rows_past_the_range_of_their_squares(d, rot):
     """Magnitudes of 1e20 and more: rstd 0, and with it the outputs and every gradient; the other

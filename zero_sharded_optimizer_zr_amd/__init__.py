@@ -853,21 +853,24 @@ class TensorList:
 
     def __init__(self, tensors: Sequence[torch.Tensor]):
         self.tensors = tuple(tensors)
-        self.device = self.dtype = None
+        self.dtype = device = None
+        ptrs, numels = [], []
         for i, t in enumerate(self.tensors):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"tensors[{i}] must be a torch.Tensor")
-            _typed(t, _DTYPES, f"tensors[{i}]")
+            if i == 0:
+                _typed(t, _DTYPES, "tensors[0]")
+                self.dtype, device = t.dtype, t.get_device()
+            elif t.dtype != self.dtype:
+                raise TypeError(f"tensors[{i}] is {t.dtype}, the tensors before it {self.dtype}")
+            elif t.get_device() != device:
+                raise ValueError(f"tensors[{i}] is on {t.device}, the tensors before it on {self.tensors[0].device}")
             if not t.is_contiguous():
                 raise ValueError(f"tensors[{i}] must be contiguous")
-            if i and t.dtype != self.dtype:
-                raise TypeError(f"tensors[{i}] is {t.dtype}, the tensors before it {self.dtype}")
-            if i and t.device != self.device:
-                raise ValueError(f"tensors[{i}] is on {t.device}, the tensors before it on {self.device}")
-            self.dtype, self.device = t.dtype, t.device
-        n = len(self.tensors)
-        self.ptrs = (ctypes.c_void_p * max(1, n))(*[t.data_ptr() or None for t in self.tensors])
-        self.numels = (ctypes.c_int64 * max(1, n))(*[t.numel() for t in self.tensors])
+            ptrs.append(t.data_ptr() or None)
+            numels.append(t.numel())
+        n = max(1, len(ptrs))
+        self.ptrs, self.numels = (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*numels)
 
     def __len__(self):
         return len(self.tensors)
