@@ -790,8 +790,8 @@ zr_status check_rope(const char *who, zr_dtype dtype, int64_t tokens, int64_t he
 {
     if (dtype != ZR_BF16 && dtype != ZR_F16)
         return fail(ZR_EINVAL, "%s: dtype = %d, must be ZR_BF16 or ZR_F16", who, dtype);
-    if (tokens < 0 || tokens > (int64_t)1 << 48 || head_dim < 1 || head_dim > ZR_MAX_HEAD_DIM)
-        return fail(ZR_EINVAL, "%s: tokens outside [0, 2^48] or head_dim outside [1, %d]", who, ZR_MAX_HEAD_DIM);
+    if (tokens < 0 || tokens > (int64_t)1 << 40 || head_dim < 1 || head_dim > ZR_MAX_HEAD_DIM)
+        return fail(ZR_EINVAL, "%s: tokens outside [0, 2^40] or head_dim outside [1, %d]", who, ZR_MAX_HEAD_DIM);
     if (!(eps >= 0.0) || !std::isfinite(eps) || !std::isfinite((float)eps))
         return fail(ZR_EINVAL, "%s: eps must be finite and >= 0", who);
     if ((q && (q->heads < 0 || q->heads > 65536)) || (k && (k->heads < 0 || k->heads > 65536)))
@@ -889,16 +889,10 @@ void divide_backward(RopeArgs *a, const int64_t (&steps)[2], int64_t waves)
             }
             return parts[0] + parts[1];
         };
-        int64_t low = 1, high = 8;
-        while (needed(high) > kGradParts)
-            high *= 2;
-        while (low < high) {
-            const int64_t middle = low + (high - low) / 2;
-            if (needed(middle) > kGradParts)
-                low = middle + 1;
-            else
-                high = middle;
-        }
+        // from what an even division would give, up in steps of at most a 500th
+        int64_t low = 1 + (units[0] * (2 * per[0] + 1) + units[1] * (2 * per[1] + 1)) / (kGradParts * waves);
+        while (needed(low) > kGradParts && (best == 0 || low < best))
+            low += 1 + low / 512;
         if (best == 0 || low < best) {
             best = low;
             needed(low);
