@@ -546,7 +546,7 @@ constexpr int kRopeGradThreads = 256;
 // takes every parts * 4'th unit and sums the weight gradient of its lanes' chunks over them.
 // The next step's rows, of the next unit too, are asked for before the present ones are
 // worked on; two steps ahead (107 us), or 12 waves to a compute unit for 8 (105), were slower.
-// 16384 tokens of 40 heads of 128: 95 us, 5.3 TB/s, and 4.5 for the sums of the sums.
+// 16384 tokens of 40 heads of 128: 96 us, 5.2 TB/s, and 5 for the sums of the sums.
 template <typename T, int V, int kLanes, int kChunks, bool kRagged>
 __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
 {
