@@ -511,9 +511,11 @@ ZR_API zr_status zr_offload_adamw_step(const void *grad, float *master, float *e
  *
  * Buffers, sizes, layouts and the fp16 loss-scale record are fixed at
  * capture; the AdamW hyper-parameters (step t, lr, ...) of every recorded
- * AdamW-family call (zr_adamw_step, zr_reduce_adamw_step, zr_adamw_step_f16)
- * are replaced by zr_graph_set_adamw, which affects the following launches
- * (until then the captured values apply).  A replay gives the same bits as
+ * AdamW-family call (zr_adamw_step, zr_reduce_adamw_step, zr_adamw_step_f16 and
+ * the clipped forms of zr_clip.h) are replaced by zr_graph_set_adamw, which affects
+ * the following launches (until then the captured values apply).  grad_scale
+ * reaches the captured gradient norm too, as zr_clip.h describes; what else the
+ * norm takes is fixed at capture.  A replay gives the same bits as
  * the eager calls.  The calls are validated at capture time, as usual, and
  * enqueue nothing then.  zr_offload_adamw_step synchronises with the host and
  * cannot be recorded.  Launching the same graph on two streams at once races.

@@ -68,6 +68,10 @@ typedef struct zr_clip_hparams {
  * contents undefined before and after; two calls that may run at once need workspaces and
  * records of their own, and so do two graphs whose replays may.  The tensors may overlap
  * one another (each counts), not the record, the workspace or ls.
+ * In a captured step: zr_graph_set_adamw gives its grad_scale to every zr_grad_norm that was
+ * captured with the grad_scale of an AdamW-family call of the same graph (compared as
+ * doubles), so that the norm stays that of the step's gradient.  A norm captured with
+ * another scale keeps it; max_norm and eps are fixed at capture.
  * Errors: ZR_EINVAL, ZR_EALIGN, ZR_EHIP.
  */
 ZR_API zr_status zr_grad_norm(const void *const *grads, const int64_t *numels, int32_t n, zr_dtype dtype,
@@ -88,8 +92,8 @@ ZR_API zr_status zr_clip_grads(void *const *grads, const int64_t *numels, int32_
  * factor (one fp64 product) in the place of grad_scale, bit for bit.  The clipped
  * gradient is not written: clipping costs the step no pass over memory.  A factor of NaN
  * makes every state NaN, as a gradient of NaN does; only the fp16 form skips such a step.
- * The graph calls of zr.h treat it as a call of the AdamW family.  Buffer rules as zr_adamw_step; the
- * record must not overlap a buffer.  Errors: ZR_EINVAL, ZR_EALIGN, ZR_EHIP.
+ * The graph calls of zr.h treat it as a call of the AdamW family.  Buffer rules as
+ * zr_adamw_step; the record must not overlap a buffer.  Errors: ZR_EINVAL, ZR_EALIGN, ZR_EHIP.
  */
 ZR_API zr_status zr_adamw_step_clip(const void *grad, float *master, float *exp_avg, float *exp_avg_sq,
                                     void *param_out, int64_t numel, const zr_adamw_hparams *hp, const zr_clip *clip,

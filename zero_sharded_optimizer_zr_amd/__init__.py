@@ -635,7 +635,8 @@ def zr_graph_info(g: Graph) -> Tuple[int, int]:
 
 def zr_graph_set_adamw(g: Graph, *, lr: float, beta1: float, beta2: float, eps: float, weight_decay: float,
                        step: int, grad_scale: float = 1.0) -> None:
-    """AdamW hyper-parameters for the graph's following launches."""
+    """AdamW hyper-parameters for the graph's following launches; grad_scale also for the
+    gradient norms that were captured with a step's grad_scale (zr_clip.h)."""
     hp = _HParams(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), float(grad_scale),
                   int(step))
     _check(_lib.zr_graph_set_adamw(g.handle, ctypes.byref(hp)))

@@ -12,9 +12,9 @@
 #include <algorithm>
 #include <new>
 
+#include "clip.hpp"
 #include "fp16.hpp"
 #include "fp8.hpp"
-#include "zr_clip.h"
 
 namespace zr {
 
@@ -69,13 +69,6 @@ struct Lookup {
 };
 
 // ------------------------------------------------------------------- norm ----
-
-struct NormFinish {
-    double max_norm, eps, grad_scale;
-    int32_t accumulate;
-    zr_loss_scale *ls;
-    zr_clip *clip;
-};
 
 struct F32 {};
 
@@ -416,6 +409,15 @@ int clip_scalar_slots(ScalarSlot *out)
     out[4] = slot_of(adamw_clip_scalar_kernel<StepBF16>);
     out[5] = slot_of(adamw_clip_scalar_kernel<StepF16>);
     return 6;
+}
+
+int norm_finish_slots(ScalarSlot *out)
+{
+    out[0] = slot_of<NormFinish>(norm_finish_kernel);
+    out[1] = slot_of<NormFinish>(norm_one_kernel<BF16>);
+    out[2] = slot_of<NormFinish>(norm_one_kernel<F16>);
+    out[3] = slot_of<NormFinish>(norm_one_kernel<F32>);
+    return 4;
 }
 
 namespace {

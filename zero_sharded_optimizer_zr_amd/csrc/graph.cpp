@@ -7,30 +7,31 @@
 // (AdamWScalars), so the graph keeps, for every captured kernel node that
 // takes it, the node and its argument list, and zr_graph_set_adamw rewrites
 // that one argument on the instantiated graph (hipGraphExecKernelNodeSetParams)
-// before the next replay.  Everything else -- buffers, sizes, layout
+// before the next replay.  A captured gradient norm holds the step's grad_scale
+// too: where it was captured with a step's, it is rewritten with it, or the step
+// would be bounded by the norm at the old scale.  Everything else -- buffers, sizes, layout
 // descriptors, the fp16 loss-scale record -- is fixed at capture.
+#include <algorithm>
 #include <new>
 #include <vector>
 
-#include "zr_math.hpp"
+#include "clip.hpp"
 
 struct zr_graph {
     hipGraph_t graph = nullptr;
     hipGraphExec_t exec = nullptr;
-    struct AdamWNode {
+    struct Node {
         hipGraphNode_t node;
         hipKernelNodeParams params;
         std::vector<void *> args;  // the captured argument pointers; args[index] is replaced
         int index;
     };
-    std::vector<AdamWNode> adamw;
+    std::vector<Node> adamw;
+    std::vector<Node> norms;  // those captured with the grad_scale of one of `adamw`
     int kernels = 0;
 };
 
 namespace zr {
-
-int clip_scalar_slots(ScalarSlot *out);  // clip.hip
-
 namespace {
 
 std::vector<ScalarSlot> all_slots()
@@ -42,6 +43,40 @@ std::vector<ScalarSlot> all_slots()
     k += clip_scalar_slots(v.data() + k);
     v.resize(k);
     return v;
+}
+
+std::vector<ScalarSlot> norm_slots()
+{
+    std::vector<ScalarSlot> v(kMaxScalarSlots);
+    v.resize(norm_finish_slots(v.data()));
+    return v;
+}
+
+// Adds the node to `nodes` if its kernel is one of the slots'.  False if it is and has
+// no argument list.
+bool keep_node(const std::vector<ScalarSlot> &slots, hipGraphNode_t node, const hipKernelNodeParams &p,
+               std::vector<zr_graph::Node> *nodes)
+{
+    for (const ScalarSlot &sl : slots) {
+        if (sl.func != p.func)
+            continue;
+        if (!p.kernelParams)
+            return false;
+        nodes->push_back({node, p, std::vector<void *>(p.kernelParams, p.kernelParams + sl.nargs), sl.index});
+        break;
+    }
+    return true;
+}
+
+// The node's argument becomes `value` in the following launches (the call copies it).
+hipError_t set_argument(hipGraphExec_t exec, const zr_graph::Node &n, void *value)
+{
+    std::vector<void *> args = n.args;
+    args[n.index] = value;
+    hipKernelNodeParams p = n.params;
+    p.kernelParams = args.data();
+    p.extra = nullptr;
+    return hipGraphExecKernelNodeSetParams(exec, n.node, &p);
 }
 
 zr_status hip_fail(const char *who, const char *what, hipError_t e)
@@ -92,7 +127,7 @@ extern "C" zr_status zr_graph_capture_end(void *stream, zr_graph **out)
     std::vector<hipGraphNode_t> nodes(count);
     if (count && (e = hipGraphGetNodes(g->graph, nodes.data(), &count)) != hipSuccess)
         return bail(hip_fail(who, "hipGraphGetNodes", e));
-    const std::vector<ScalarSlot> slots = all_slots();
+    const std::vector<ScalarSlot> slots = all_slots(), norms = norm_slots();
     for (hipGraphNode_t n : nodes) {
         hipGraphNodeType type;
         if ((e = hipGraphNodeGetType(n, &type)) != hipSuccess)
@@ -103,20 +138,15 @@ extern "C" zr_status zr_graph_capture_end(void *stream, zr_graph **out)
         hipKernelNodeParams p{};
         if ((e = hipGraphKernelNodeGetParams(n, &p)) != hipSuccess)
             return bail(hip_fail(who, "hipGraphKernelNodeGetParams", e));
-        for (const ScalarSlot &sl : slots) {
-            if (sl.func != p.func)
-                continue;
-            if (!p.kernelParams)
-                return bail(fail(ZR_EHIP, "%s: a captured AdamW node has no argument list", who));
-            zr_graph::AdamWNode a;
-            a.node = n;
-            a.params = p;
-            a.args.assign(p.kernelParams, p.kernelParams + sl.nargs);
-            a.index = sl.index;
-            g->adamw.push_back(a);
-            break;
-        }
+        if (!keep_node(slots, n, p, &g->adamw) || !keep_node(norms, n, p, &g->norms))
+            return bail(fail(ZR_EHIP, "%s: a captured AdamW or norm node has no argument list", who));
     }
+    g->norms.erase(std::remove_if(g->norms.begin(), g->norms.end(), [&](const zr_graph::Node &n) {
+        const double scale = static_cast<const NormFinish *>(n.args[n.index])->grad_scale;
+        return std::none_of(g->adamw.begin(), g->adamw.end(), [&](const zr_graph::Node &a) {
+            return static_cast<const AdamWScalars *>(a.args[a.index])->grad_scale == scale;
+        });
+    }), g->norms.end());
     if ((e = hipGraphInstantiate(&g->exec, g->graph, nullptr, nullptr, 0)) != hipSuccess)
         return bail(hip_fail(who, "hipGraphInstantiate", e));
     *out = g;
@@ -145,13 +175,15 @@ extern "C" zr_status zr_graph_set_adamw(zr_graph *g, const zr_adamw_hparams *hp)
     if (st != ZR_OK)
         return st;
     AdamWScalars s = adamw_scalars(*hp);
-    for (auto &a : g->adamw) {
-        std::vector<void *> args = a.args;
-        args[a.index] = &s;
-        hipKernelNodeParams p = a.params;
-        p.kernelParams = args.data();
-        p.extra = nullptr;
-        hipError_t e = hipGraphExecKernelNodeSetParams(g->exec, a.node, &p);  // copies the arguments
+    for (const auto &a : g->adamw) {
+        const hipError_t e = set_argument(g->exec, a, &s);
+        if (e != hipSuccess)
+            return hip_fail(who, "hipGraphExecKernelNodeSetParams", e);
+    }
+    for (const auto &n : g->norms) {
+        NormFinish f = *static_cast<const NormFinish *>(n.args[n.index]);
+        f.grad_scale = hp->grad_scale;
+        const hipError_t e = set_argument(g->exec, n, &f);
         if (e != hipSuccess)
             return hip_fail(who, "hipGraphExecKernelNodeSetParams", e);
     }

@@ -149,9 +149,9 @@ zr_status adamw_run(const uint16_t *g, float *master, float *exp_avg, float *exp
 
 // ------------------------------------------------- graph parameter slots --
 
-// A kernel that takes the per-step AdamW scalars by value, as captured graphs
-// see it: its host-side address, its argument count and the position of the
-// AdamWScalars argument (deduced from the signature at compile time).
+// A kernel that takes the per-step AdamW scalars (or the norm's, NormFinish) by
+// value, as captured graphs see it: its host-side address, its argument count and
+// the position of that argument (deduced from the signature at compile time).
 struct ScalarSlot {
     const void *func;
     int nargs;
@@ -168,11 +168,11 @@ constexpr int arg_index()
     return -1;
 }
 
-template <typename... A>
+template <typename T = AdamWScalars, typename... A>
 ScalarSlot slot_of(void (*kernel)(A...))
 {
-    static_assert(arg_index<AdamWScalars, A...>() >= 0, "kernel takes no AdamWScalars");
-    return ScalarSlot{reinterpret_cast<const void *>(kernel), (int)sizeof...(A), arg_index<AdamWScalars, A...>()};
+    static_assert(arg_index<T, A...>() >= 0, "kernel takes no such argument");
+    return ScalarSlot{reinterpret_cast<const void *>(kernel), (int)sizeof...(A), arg_index<T, A...>()};
 }
 
 // The AdamW-family kernels of each translation unit (adamw.hip, fused.hip,
