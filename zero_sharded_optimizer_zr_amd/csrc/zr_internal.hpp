@@ -33,9 +33,10 @@ void clear_error();
 void for_each_fragment(const zr_layout &L, int64_t begin, int64_t end,
                        const std::function<void(const zr_fragment &)> &fn);
 
-// Most workgroups one launch gets: what one grid dimension allows, or fewer
-// when the environment sets ZR_MAX_GRID (>= 8; a testing knob).  Every kernel
-// loops over the work its grid does not cover, so results never depend on it.
+// Most workgroups one launch asks for: 2^31 - 1, or fewer when the environment
+// sets ZR_MAX_GRID (>= 8; a testing knob); launch() holds them to what their size
+// allows.  Every kernel loops over the work its grid does not cover, so results
+// never depend on it.
 inline int64_t max_grid()
 {
     const char *s = std::getenv("ZR_MAX_GRID");
@@ -111,6 +112,17 @@ inline bool overlaps(const void *a, int64_t abytes, const void *b, int64_t bbyte
            y < x + static_cast<uintptr_t>(abytes);
 }
 
+// The grid that a launch of `block` threads a workgroup gets: HIP allows a dimension
+// fewer than 2^32 work items (2^24 - 1 workgroups of 256), and past that the kernel
+// loops.  A multiple of 8 stays one (tiles dealt to the XCDs).
+inline dim3 launch_grid(dim3 grid, dim3 block)
+{
+    const uint32_t most = 0xffffffffu / block.x / 8 * 8;
+    if (grid.x > most)
+        grid.x = most;
+    return grid;
+}
+
 // Launches `kernel` through hipLaunchKernel so the status of this launch is
 // returned directly (no sticky-error ambiguity).  `lds_bytes` of dynamic LDS is
 // reserved per workgroup; the streaming kernels never touch it and use it only
@@ -126,7 +138,8 @@ zr_status launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t lds_by
         int i = 0;
         ((ptrs[i++] = static_cast<void *>(&v)), ...);
     }, values);
-    hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(kernel), grid, block, ptrs, lds_bytes, stream);
+    hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(kernel), launch_grid(grid, block), block, ptrs,
+                                   lds_bytes, stream);
     if (e != hipSuccess)
         return fail(ZR_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
     return ZR_OK;
