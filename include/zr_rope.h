@@ -69,7 +69,7 @@ typedef struct zr_rope {
  * exactly k.  Otherwise no output may overlap another buffer; heads of one fused row
  * (equal token strides, ranges of the row that do not meet) do not count as overlapping.
  * positions: device int64 [axes][position_stride] with position_stride >= tokens where
- * axes > 1, any values.  0 <= tokens <= 2^40 (0 is a no-op), heads <= 65536, 1 <= head_dim <=
+ * axes > 1, or 0 where all axes share the first's; any values.  0 <= tokens <= 2^40 (0 is a no-op), heads <= 65536, 1 <= head_dim <=
  * ZR_MAX_HEAD_DIM, eps finite and >= 0.  positions may be NULL where rot_dim is 0.
  * Errors: ZR_EINVAL, ZR_EALIGN, ZR_EHIP.
  */

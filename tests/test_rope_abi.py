@@ -113,6 +113,20 @@ def test_calls_without_work():
     assert call("zr_qk_norm_rope_backward", BACKWARD, dq=None, dk=none, **nothing) == 0
 
 
+@pytest.mark.parametrize("fn,base", [("zr_qk_norm_rope", FORWARD), ("zr_qk_norm_rope_backward", BACKWARD)])
+def test_positions_that_all_axes_share(fn, base):
+    """A distance of 0 is no refusal, one between 0 and the tokens is; the shared row counts as a
+    buffer (the outputs over its first and its last position)."""
+    out = "k_out" if fn == "zr_qk_norm_rope" else "dk_in"
+    shared = dict(rope=rope(axes=3, axis=[0, 1, 2, 0, 1, 2, 0, 1]), position_stride=0)
+    for stride in (1, T - 1, -1):
+        assert call(fn, base, **{**shared, "position_stride": stride}) == 1
+        assert "position_stride" in zr.zr_last_error()
+    for off in (0, T * 8 - 2):
+        assert call(fn, base, **shared, **{out: heads(4, HK, off=off)}) == 1
+        assert "overlaps" in zr.zr_last_error()
+
+
 # ------------------------------------------------------------------- binding ----
 
 def tensors(t=3):

@@ -1057,9 +1057,9 @@ def zr_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weig
                     stream=None) -> None:
     """q_out, k_out [tokens, heads, head_dim] = the heads of q, k divided by their root mean
     square, times q_weight, k_weight [head_dim] (None: not normed), and turned by their
-    positions (int64 [tokens], or [axes, tokens] for rope's axes).  q or k may be None; q_out
-    may be q, k_out k.  Tokens and heads may have any strides (slices of the fused
-    product's rows)."""
+    positions (int64 [tokens], or [axes, tokens] for rope's axes, which an expanded view may
+    be).  q or k may be None; q_out may be q, k_out k.  Tokens and heads may have any strides
+    at which rows do not overlap (slices of the fused product's rows; no expanded heads)."""
     kind, tokens, dim = _qk(q, k)
     (c_q, hq), (c_k, hk) = _heads(q, kind, tokens, None, dim, "q"), _heads(k, kind, tokens, None, dim, "k")
     c_qo, c_ko = _heads(q_out, kind, tokens, hq, dim, "q_out")[0], _heads(k_out, kind, tokens, hk, dim, "k_out")[0]

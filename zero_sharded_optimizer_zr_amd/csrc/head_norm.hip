@@ -815,9 +815,9 @@ zr_status check_rope(const char *who, zr_dtype dtype, int64_t tokens, int64_t he
         if (!aligned_to(positions, 8) || !aligned_to(rope->inv_freq, 4))
             return fail(ZR_EALIGN, "%s: positions must be 8-byte and inv_freq 4-byte aligned", who);
         int64_t n;
-        if (rope->axes > 1 && (position_stride < tokens ||
+        if (rope->axes > 1 && ((position_stride != 0 && position_stride < tokens) ||
                                __builtin_mul_overflow((int64_t)rope->axes, position_stride, &n) || n > INT64_MAX / 8))
-            return fail(ZR_EINVAL, "%s: position_stride below tokens, or positions past int64", who);
+            return fail(ZR_EINVAL, "%s: position_stride below tokens and not 0, or positions past int64", who);
     }
     return ZR_OK;
 }
