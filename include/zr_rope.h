@@ -65,8 +65,8 @@ typedef struct zr_rope {
 /*
  * q_out, k_out = norm and rotation of q, k (dtype ZR_BF16 or ZR_F16; q_weight and
  * k_weight [head_dim] of the same type, or NULL: that tensor is turned and not normed).
- * q_out and k_out have the heads of q and k; q_out may be exactly q (same strides), k_out
- * exactly k.  Otherwise no output may overlap another buffer; heads of one fused row
+ * q_out and k_out have the heads of q and k; q_out may be exactly q (same strides along the
+ * axes longer than 1), k_out exactly k.  Otherwise no output may overlap another buffer; heads of one fused row
  * (equal token strides, ranges of the row that do not meet) do not count as overlapping.
  * positions: device int64 [axes][position_stride] with position_stride >= tokens where
  * axes > 1, or 0 where all axes share the first's; any values.  0 <= tokens <= 2^40 (0 is a no-op), heads <= 65536, 1 <= head_dim <=

@@ -991,9 +991,11 @@ zr_status for_layout(RopeArgs *a, hipStream_t st)
 }
 
 int64_t heads_of(const zr_heads *h) { return h ? h->heads : 0; }
-bool same_heads(const zr_heads *a, const zr_heads *b)
+// Whether two tensors' rows are the same ones: the distance along an axis of length 1 says nothing.
+bool same_heads(const zr_heads *a, const zr_heads *b, int64_t tokens)
 {
-    return a && b && a->ptr == b->ptr && a->token_stride == b->token_stride && a->head_stride == b->head_stride;
+    return a && b && a->ptr == b->ptr && (tokens <= 1 || a->token_stride == b->token_stride) &&
+           (a->heads <= 1 || a->head_stride == b->head_stride);
 }
 
 }  // namespace
@@ -1029,7 +1031,8 @@ extern "C" zr_status zr_qk_norm_rope(const zr_heads *q, const zr_heads *k, const
     c[7] = {turned ? rope->inv_freq : nullptr, 2 * rope->rot_dim, 0, 0};
     for (int i = 0; i < 2; ++i)
         for (int j = i + 1; j < 8; ++j) {
-            const bool in_place = (i == 0 && j == 2 && same_heads(q_out, q)) || (i == 1 && j == 3 && same_heads(k_out, k));
+            const bool in_place = (i == 0 && j == 2 && same_heads(q_out, q, tokens)) ||
+                                  (i == 1 && j == 3 && same_heads(k_out, k, tokens));
             if (!in_place && meet(c[i], c[j]))
                 return fail(ZR_EINVAL, "%s: an output overlaps another buffer", who);
         }
@@ -1088,8 +1091,9 @@ extern "C" zr_status zr_qk_norm_rope_backward(const zr_heads *dq, const zr_heads
     c[12] = {turned ? rope->inv_freq : nullptr, 2 * rope->rot_dim, 0, 0};
     for (int i = 0; i < 5; ++i)
         for (int j = i + 1; j < 13; ++j) {
-            const bool in_place = (i == 0 && ((j == 5 && same_heads(dq_in, dq)) || (j == 7 && same_heads(dq_in, q)))) ||
-                                  (i == 1 && ((j == 6 && same_heads(dk_in, dk)) || (j == 8 && same_heads(dk_in, k))));
+            const bool in_place =
+                (i == 0 && ((j == 5 && same_heads(dq_in, dq, tokens)) || (j == 7 && same_heads(dq_in, q, tokens)))) ||
+                (i == 1 && ((j == 6 && same_heads(dk_in, dk, tokens)) || (j == 8 && same_heads(dk_in, k, tokens))));
             if (!in_place && meet(c[i], c[j]))
                 return fail(ZR_EINVAL, "%s: an output overlaps another buffer", who);
         }
