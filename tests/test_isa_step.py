@@ -78,3 +78,25 @@ def test_head_rows(asm, kernel, width, loads):
     out = [ln for ln in ops if ln.startswith(f"global_store_{width}")]
     assert out and all(ln.rstrip().endswith(" nt") for ln in out)
     assert not [ln for ln in ops if ln.startswith(("flat_load", "flat_store", "scratch_"))]
+
+
+@pytest.mark.parametrize("src", SOURCES)
+def test_memory_is_written_by_vector_and_lds_instructions_alone(asm, src):
+    """Every store and every atomic is a global_ or a ds_ one (scratch_ where a kernel spills, which
+    the next test bounds), and nothing acts on the scalar cache but its loads."""
+    ops = {ln.split()[0] for ln in asm[src].splitlines() if re.match(r"\s+[a-z]\w+", ln)}
+    writes = {op for op in ops if "store" in op or "atomic" in op or "write" in op}
+    allowed = ("global_store_", "ds_", "v_writelane_", "scratch_store_")
+    assert any(op.startswith("global_store_") for op in writes)
+    assert not [op for op in writes if not op.startswith(allowed)]
+    assert not [op for op in ops if "dcache" in op]
+
+
+@pytest.mark.parametrize("src", SOURCES)
+def test_scratch_of_the_one_spilling_kernel(asm, src):
+    """Only the backward kernel of single elements, four chunks to a lane, has scratch, and 32 bytes at most."""
+    sizes = re.findall(r"\.name:\s+(\S+).*?\.private_segment_fixed_size:\s+(\d+)", asm[src], re.S)
+    assert sizes
+    for name, size in sizes:
+        spills = "rope_grad_kernel" in name and "Li1ELi64ELi4E" in name
+        assert int(size) <= (32 if spills else 0), (name, size)
