@@ -317,6 +317,35 @@ def test_infinities_stay_in_their_row():
     assert not out.any()
 
 
+@pytest.mark.parametrize("d,rot", [(128, 128), (66, 66), (33, 18)])
+def test_gradients_of_rows_with_infinities(d, rot):
+    """An infinity in a row of x makes its gradients NaN and the weight's at its own column (the others
+    get nothing of the row: its rstd is 0); a NaN makes all of the weight's NaN.  An infinite gradient makes
+    the row's NaN.  The other rows are as without them."""
+    device()
+    c = case(12, 6, 2, d, rot, BF)
+    dy = [torch.randn(c[x].shape, device="cuda").to(BF) for x in "qk"]
+    clean = backward_of(c, dy)
+    c["q"][7, 5] = 0.0
+    zeroed = backward_of(c, dy)[2]
+    keep = torch.ones(12, 6, dtype=torch.bool, device="cuda")
+    keep[7, 5] = False
+    for value in (inf, -inf, nan):
+        c["q"][7, 5] = 1.0
+        c["q"][7, 5, 3] = value
+        dq, dk, dwq, dwk = backward_of(c, dy)
+        assert bool(dq[~keep].isnan().all()) and torch.equal(dq[keep], clean[0][keep])
+        assert torch.equal(dk, clean[1]) and torch.equal(dwk, clean[3])
+        other = torch.arange(d, device="cuda") != 3
+        assert bool(dwq[3].isnan())
+        assert bool(dwq.isnan().all()) if value != value else torch.equal(dwq[other], zeroed[other])
+    c["q"][7, 5] = 1.0
+    dy[0][7, 5, 0] = inf
+    dq, dk, _, dwk = backward_of(c, dy)
+    assert not bool(dq[~keep].isfinite().any()) and torch.equal(dq[keep], clean[0][keep])
+    assert torch.equal(dk, clean[1]) and torch.equal(dwk, clean[3])
+
+
 @pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-31, 1e-6, 3.0])
 def test_eps(eps):
     """Both ways of the reciprocal root.  Values of 1e-12 (squares of 1e-24) and of 1: the
