@@ -58,7 +58,8 @@ typedef struct zr_clip_hparams {
  *   factor = min(1, max_norm / (norm + eps))
  * worked out in fp64 and rounded once to fp32.  Clipping by the global norm: Pascanu,
  * Mikolov & Bengio, ICML 2013.  An infinity among the elements makes the norm infinite and the
- * factor 0, a NaN makes both NaN; finite elements never overflow the sum.  With ls,
+ * factor 0, a NaN makes both NaN (with max_norm infinite the factor is 1 whatever the norm is);
+ * finite elements never overflow the sum.  With ls,
  * ls->found_inf is set if the sum is not finite, so that the fp16 step is skipped -- on
  * every rank, once the sum has been all-reduced.
  *

@@ -18,8 +18,11 @@
  *
  * The angle is an fp64 product, reduced to one turn in fp64 before its sine and cosine
  * are taken in fp32: positions of 2^31 at a frequency of 1 still have angles right to 2^-20.
- * All other arithmetic is fp32, each output rounded once; a row whose squares pass fp32's
- * range (magnitudes from about 1e19 on) has rstd 0, and outputs and gradients 0 with it.
+ * All other arithmetic is fp32, each output rounded once; a finite row whose squares pass
+ * fp32's range (magnitudes from about 1e19 on) has rstd 0, and outputs and gradients 0 with
+ * it.  An infinity or a NaN in a normed row makes NaN where the formulas do, in that row and
+ * in the weight's gradient.  Squares below fp32's normal range (magnitudes under about 1e-19)
+ * lose bits or count as zeros: rows of them take an eps well above 1e-38.
  *
  * The conventions of zr.h hold for every call: validation first, nothing launched and
  * nothing written on an error, asynchronous on `stream`, no device allocation,
@@ -69,8 +72,9 @@ typedef struct zr_rope {
  * axes longer than 1), k_out exactly k.  Otherwise no output may overlap another buffer; heads of one fused row
  * (equal token strides, ranges of the row that do not meet) do not count as overlapping.
  * positions: device int64 [axes][position_stride] with position_stride >= tokens where
- * axes > 1, or 0 where all axes share the first's; any values.  0 <= tokens <= 2^40 (0 is a no-op), heads <= 65536, 1 <= head_dim <=
- * ZR_MAX_HEAD_DIM, eps finite and >= 0.  positions may be NULL where rot_dim is 0.
+ * axes > 1, or 0 where all axes share the first's; any values.  0 <= tokens <= 2^40 (0 is a
+ * no-op), heads <= 65536, 1 <= head_dim <= ZR_MAX_HEAD_DIM, eps finite and >= 0.  positions
+ * may be NULL where rot_dim is 0.
  * Errors: ZR_EINVAL, ZR_EALIGN, ZR_EHIP.
  */
 ZR_API zr_status zr_qk_norm_rope(const zr_heads *q, const zr_heads *k, const void *q_weight, const void *k_weight,

@@ -849,8 +849,10 @@ ZR_GRAD_NORM_PARTIALS = 2048
 
 class TensorList:
     """Tensors of one dtype and device, as zr_grad_norm and zr_clip_grads take them: made
-    once (tensor_list) and kept, it spares those calls the checks of every tensor.  It
-    holds the tensors; their memory must stay where it is (no resize_ or set_)."""
+    once (tensor_list) and kept, it spares those calls the checks of every tensor (about 0.4 us
+    of the host's time for each: 24 us for 65 tensors beside a call of 9), which a call on a plain
+    sequence makes every time.  It holds the tensors; their memory must stay where it is (no
+    resize_ or set_)."""
 
     def __init__(self, tensors: Sequence[torch.Tensor]):
         self.tensors = tuple(tensors)
@@ -908,7 +910,7 @@ def zr_grad_norm(grads: Union[TensorList, Sequence[torch.Tensor]], clip: torch.T
                  ls: Optional[torch.Tensor] = None, stream=None) -> None:
     """clip <- the sum of squares of all elements of grads (added to what it holds with
     accumulate), norm = |grad_scale| * sqrt(sum) / ls's scale and factor = min(1, max_norm /
-    (norm + eps)).  ls (fp16 gradients) gets its overflow flag set if the sum is not finite.
+    (norm + eps)), 1 without a max_norm.  ls (fp16 gradients) gets its overflow flag set if the sum is not finite.
     Ranks that each hold a part all-reduce clip[:1] and call again with accumulate and the
     tensors that all hold, or none."""
     grads = _list(grads)

@@ -332,8 +332,10 @@ __device__ __forceinline__ void adamw_clip_one(const uint16_t *grad, float *mast
 
 // The AdamW kernel of 4 elements to a lane (28 bytes an element, seven streams), its
 // factor read from the record.  The record's load is issued before the data's and first
-// used behind it: the empty asm takes both together.  1.05e8 elements: 472 us, 6.2 TB/s, beside
-// 469 us for the kernel without a record on the same buffers, in bf16 and in fp16.
+// used behind it: the empty asm takes both together.  1.05e8 elements, in turn with the kernel
+// without a record on the same buffers (medians of a kernel trace): 474 us, 6.2 TB/s, beside 466 in
+// bf16, 476 beside 475 in fp16; called on one set of buffers 467 beside 463, and 472 beside 469.
+// Either kernel takes up to a quarter longer in its first fifty launches behind an idle time.
 template <typename T, bool kParam>
 __global__ __launch_bounds__(kBlock) void adamw_clip_vec_kernel(const uint16_t *grad, float *master, float *m, float *v,
                                                                 uint16_t *param, int64_t numel, int64_t head,

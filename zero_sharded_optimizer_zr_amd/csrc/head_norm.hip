@@ -546,7 +546,7 @@ constexpr int kRopeGradThreads = 256;
 // takes every parts * 4'th unit and sums the weight gradient of its lanes' chunks over them.
 // The next step's rows, of the next unit too, are asked for before the present ones are
 // worked on; two steps ahead (107 us), or 12 waves to a compute unit for 8 (105), were slower.
-// 16384 tokens of 40 heads of 128: 96 us, 5.2 TB/s, and 5 for the sums of the sums.
+// 16384 tokens of 40 heads of 128: 97 us, 5.2 TB/s, and 5 for the sums of the sums.
 template <typename T, int V, int kLanes, int kChunks, bool kRagged>
 __global__ __launch_bounds__(kRopeGradThreads) void rope_grad_kernel(RopeArgs a)
 {
@@ -842,6 +842,10 @@ void fill_args(RopeArgs *a, int64_t tokens, int64_t head_dim, double eps, const 
         a->axis[j] = rope->pair_axis && j < rope->rot_dim / 2 ? rope->pair_axis[j] : 0;
 }
 
+// Steps of a call up to which a wave takes one.  Replayed graphs, 32 + 8 heads of 128, one step to a
+// wave and up to four: 160 steps 3.1 us and 4.0, 1280 3.5 and 4.1, 2050 3.8 and 4.2, 4000 4.5 and 4.7,
+// 5120 4.9 and 4.7, 20480 12.4 and 9.1 (heads of 80 and of 64 the same): they cross between 4000
+// and 5000.
 constexpr int64_t kFewSteps = 2048;
 
 template <typename T, int V, int kLanes, int kChunks, bool kRagged, int kSteps>
@@ -961,12 +965,14 @@ zr_status vector_launch(RopeArgs *a, int32_t lanes, hipStream_t st)
 constexpr int64_t kFewBackward = 4096;
 
 // Forward, vectors of 4 elements leave room for 7 waves to a SIMD where those of 8 leave 4
-// (5003 tokens of 24 heads of 96: 12.4 us and 14.9; 16384 of 40 of 128: 57.7 and 57.3).
-// Backward, where sums stay in registers anyway, 8 take half as many steps (99 us and 118), but
-// where those are few, what counts is how long one takes, and the sums behind it (64 tokens of
-// 40 heads of 128 in a replayed graph 8.2 us and 6.4, 777 11.1 and 11.2, 2048 19.5 and 22.0).
+// (replayed graphs: 5003 tokens of 24 heads of 96 13.4 us and 15.6; 16384 of 40 of 128 58.1 and 65.9).
+// Backward, where sums stay in registers anyway, 8 take half as many steps (124 us with 4, 98 with 8),
+// but where those are few, what counts is how long one takes, and the sums behind it (40 heads of
+// 128, with 8 and with 4: 64 tokens 8.2 us and 6.7, 777 12.5 and 12.9, 2048 19.6 and 22.7).
 // What those do not fit (65 chunks forward; parts shorter than a vector) takes the other
-// kind, heads too short for both single elements.
+// kind, heads too short for both single elements: 16384 tokens of 40 heads of 128 of which 6
+// elements are turned 129 us forward, 2.6 TB/s, and 376 backward; 4096 of 256, 90 and 158 (three sets
+// of buffers in turn).
 template <typename T, bool kForward>
 zr_status for_layout(RopeArgs *a, hipStream_t st)
 {
